@@ -198,6 +198,44 @@ struct AttnClips {
 cudaError_t launch_attention_varlen(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmVt,
                                     const AttnClips& clips, int H, __half* out, int* err, cudaStream_t st);
 
+// ------------------------------------------------------------------- training
+// Attention for training (w2v_train.h): checked sizes and strides, in elements.
+struct AttnTrain {
+  bool bf16 = false;
+  int batch = 0, T = 0, H = 0;
+  int64_t qkv_ld = 0, qkv_bs = 0, out_ld = 0, out_bs = 0, grad_ld = 0, grad_bs = 0;
+  const int32_t* frames = nullptr;
+};
+cudaError_t launch_attention_fwd(const AttnTrain& s, const void* q, const void* k, const void* v, void* out,
+                                 float* lse, int* err, cudaStream_t st);
+// ws: attention_bwd_ws_bytes(...) bytes.
+size_t attention_bwd_ws_bytes(int batch, int T, int H);
+cudaError_t launch_attention_bwd(const AttnTrain& s, const void* dout, const void* q, const void* k, const void* v,
+                                 const void* out, const float* lse, void* dq, void* dk, void* dv, void* ws, int* err,
+                                 cudaStream_t st);
+
+// LayerNorm for training: row types in w2v_train.h's codes, strides in elements.
+struct LnTrain {
+  int x_type = 0, y_type = 0;
+  int64_t rows = 0;
+  int cols = 0;
+  int64_t x_ld = 0, y_ld = 0;
+  const float* gamma = nullptr;
+  const float* beta = nullptr;
+  int act = 0;
+};
+cudaError_t launch_layernorm_fwd(const LnTrain& s, const void* x, void* y, float eps, float* mean, float* rstd,
+                                 cudaStream_t st);
+size_t layernorm_bwd_ws_bytes(int64_t rows, int cols);
+cudaError_t launch_layernorm_bwd(const LnTrain& s, const void* dy, const void* x, const float* mean,
+                                 const float* rstd, const void* dres, int64_t dres_ld, void* dx, int64_t dx_ld,
+                                 float* dgamma, float* dbeta, void* ws, cudaStream_t st);
+
+// Gradient norm and clipping over n tensors (host arrays).
+size_t grad_clip_ws_bytes(int n);
+cudaError_t launch_grad_clip(int n, const void* const* grads, void* const* outs, const int64_t* counts,
+                             const int* types, float scale, float max_norm, float* norm, void* ws, cudaStream_t st);
+
 // ----------------------------------------------------------------------- CTC
 cudaError_t launch_argmax(const float* logits, int rows, int V, int32_t* ids, cudaStream_t st);
 cudaError_t launch_ctc_collapse(const int32_t* ids, int batch, int T, int t_valid, int blank, int32_t* tokens,

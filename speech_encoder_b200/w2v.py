@@ -35,6 +35,15 @@ class w2v_config(ctypes.Structure):
     ]
 
 
+class w2v_attention_shape(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("batch", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
+        ("qkv_ld", ctypes.c_int64), ("qkv_bs", ctypes.c_int64), ("out_ld", ctypes.c_int64),
+        ("out_bs", ctypes.c_int64), ("grad_ld", ctypes.c_int64), ("grad_bs", ctypes.c_int64),
+        ("frames", ctypes.c_void_p),
+    ]
+
+
 class w2v_kernel_time(ctypes.Structure):
     _fields_ = [("klass", ctypes.c_int), ("ms", ctypes.c_float), ("flops", ctypes.c_double),
                 ("bytes", ctypes.c_double)]
@@ -42,6 +51,7 @@ class w2v_kernel_time(ctypes.Structure):
 
 _lib: Optional[ctypes.CDLL] = None
 VP, I, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+I64, F = ctypes.c_int64, ctypes.c_float
 
 
 def lib() -> ctypes.CDLL:
@@ -85,6 +95,15 @@ def lib() -> ctypes.CDLL:
         "w2v_op_wait_probe": (I, [VP, ctypes.c_uint64, VP]),
         "w2v_op_pointwise": (I, [I, VP, I, ctypes.c_float, ctypes.c_float, VP, VP]),
         "w2v_fold_layernorm_linear": (I, [VP, I, I, VP, VP, VP, VP, VP, VP]),
+        "w2v_op_attention_fwd": (I, [ctypes.POINTER(w2v_attention_shape)] + [VP] * 7),
+        "w2v_op_attention_bwd_workspace": (SZ, [I, I, I]),
+        "w2v_op_attention_bwd": (I, [ctypes.POINTER(w2v_attention_shape)] + [VP] * 10 + [SZ, VP, VP]),
+        "w2v_op_layernorm_fwd": (I, [VP, I, I64, VP, I, I64, I64, I, VP, VP, F, I, VP, VP, VP]),
+        "w2v_op_layernorm_bwd_workspace": (SZ, [I64, I]),
+        "w2v_op_layernorm_bwd": (I, [VP, I, I64, VP, I, I64, I64, I, VP, VP, VP, VP, I, VP, I64, VP, I64, VP, VP, VP,
+                                     SZ, VP]),
+        "w2v_op_grad_clip_workspace": (SZ, [I]),
+        "w2v_op_grad_clip": (I, [I, VP, VP, VP, VP, F, F, VP, VP, SZ, VP]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -333,6 +352,166 @@ def w2v_op_pointwise(fn: int, x, y, c: float = 1.0, b: float = 0.0, stream=None)
 
 def w2v_op_wait_probe(err, limit_ns: int, stream=None) -> int:
     return lib().w2v_op_wait_probe(_ptr(err), int(limit_ns), _stream(stream))
+
+
+# ------------------------------------------------------ operators for training
+# (include/w2v_train.h).  Tensors are checked here, since a shape or a device
+# cannot be seen from a pointer; errors raise W2VError.
+
+
+def _require(cond: bool, what: str):
+    if not cond:
+        raise W2VError(W2V_EINVAL, what)
+
+
+def _type_code(dtype) -> int:
+    import torch
+    code = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}.get(dtype)
+    _require(code is not None, f"element type {dtype}")
+    return code
+
+
+def _on_current_device(what: str, *tensors):
+    import torch
+    _require(all(t.is_cuda for t in tensors), f"{what}: a tensor is not on the GPU")
+    cur = torch.cuda.current_device()
+    _require(all(t.get_device() == cur for t in tensors), f"{what}: a tensor is not on the current device")
+
+
+def _workspace(ws, nbytes: int, device, stream):
+    """The caller's workspace, or one from torch's allocator, owned by the stream that the call runs on."""
+    import torch
+    if ws is not None:
+        _require(ws.is_contiguous() and ws.device == device, "workspace: not contiguous, or on another device")
+        return ws, ws.numel() * ws.element_size()
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+
+
+def _row_strides(what: str, *tensors):
+    """(row, clip) strides shared by [batch, T, H*64] tensors whose last axis is contiguous."""
+    batch, T, width = tensors[0].shape
+    strides = None
+    for t in tensors:
+        _require(t.shape == tensors[0].shape and t.dtype == tensors[0].dtype, f"{what}: shapes or types differ")
+        _require(t.stride(2) == 1, f"{what}: the last axis is not contiguous")
+        ld = width if T == 1 else t.stride(1)
+        bs = T * max(ld, width) if batch == 1 else t.stride(0)
+        _require(strides in (None, (ld, bs)), f"{what}: strides differ")
+        strides = (ld, bs)
+    return strides
+
+
+def _attention_shape(qkv, outs, grads, lse, err, frames) -> w2v_attention_shape:
+    q = qkv[0]
+    _require(q.dim() == 3 and q.shape[2] > 0 and q.shape[2] % 64 == 0, "attention: q is not [batch, T, H * 64]")
+    import torch
+    batch, T, width = q.shape
+    _on_current_device("attention", *qkv, *outs, *grads, lse, err, *([] if frames is None else [frames]))
+    _require(all(t.shape == q.shape and t.dtype == q.dtype for t in (*qkv, *outs, *grads)),
+             "attention: shapes or types differ")
+    _require(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (batch, width // 64, T),
+             "attention: lse is not a contiguous float32 [batch, H, T]")
+    _require(err.dtype == torch.int32 and err.numel() >= 1, "attention: err is not int32")
+    if frames is not None:
+        _require(frames.dtype == torch.int32 and frames.is_contiguous() and tuple(frames.shape) == (batch,),
+                 "attention: frames is not a contiguous int32 [batch]")
+    return w2v_attention_shape(_type_code(q.dtype), batch, T, width // 64, *_row_strides("attention q, k, v", *qkv),
+                               *_row_strides("attention out", *outs),
+                               *(_row_strides("attention gradients", *grads) if grads else (0, 0)), _ptr(frames))
+
+
+def w2v_op_attention_fwd(q, k, v, out, lse, err, frames=None, stream=None) -> None:
+    """out = softmax(q k^T / 8) v over each clip's own frames, and its log-sum-exp.
+    q, k, v (of equal strides), out: fp16 or bf16 [batch, T, H*64]; lse float32
+    [batch, H, T]; frames int32 [batch] or None (see include/w2v_train.h)."""
+    s = _attention_shape((q, k, v), (out,), (), lse, err, frames)
+    _check(lib().w2v_op_attention_fwd(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(err),
+                                      _stream(stream)), None, "w2v_op_attention_fwd")
+
+
+def w2v_op_attention_bwd_workspace(batch: int, T: int, H: int) -> int:
+    return lib().w2v_op_attention_bwd_workspace(int(batch), int(T), int(H))
+
+
+def w2v_op_attention_bwd(dout, q, k, v, out, lse, dq, dk, dv, err, frames=None, ws=None, stream=None) -> None:
+    """Writes dq, dk and dv from dout and the forward call's tensors.  out and dout
+    have equal strides, as have dq, dk and dv.  ws: a workspace of
+    w2v_op_attention_bwd_workspace bytes, or None for one from torch's allocator."""
+    s = _attention_shape((q, k, v), (out, dout), (dq, dk, dv), lse, err, frames)
+    ws, nbytes = _workspace(ws, w2v_op_attention_bwd_workspace(s.batch, s.T, s.H), q.device, stream)
+    _check(lib().w2v_op_attention_bwd(ctypes.byref(s), _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                      _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), nbytes, _ptr(err), _stream(stream)),
+           None, "w2v_op_attention_bwd")
+
+
+def _norm_rows(what: str, t, rows: int, cols: int) -> int:
+    """Row stride of a [rows, cols] tensor whose last axis is contiguous."""
+    _require(tuple(t.shape) == (rows, cols) and (cols == 1 or t.stride(1) == 1), f"layernorm: {what} is not [rows, cols]")
+    return cols if rows <= 1 else t.stride(0)
+
+
+def _norm_vectors(cols: int, rows: int, per_col, per_row):
+    import torch
+    for t, n in [(t, cols) for t in per_col] + [(t, rows) for t in per_row]:
+        _require(t.dtype == torch.float32 and t.is_contiguous() and t.numel() == n,
+                 "layernorm: a vector is not contiguous float32 of its size")
+
+
+def w2v_op_layernorm_fwd(x, y, gamma, beta, eps: float, act: int, mean, rstd, stream=None) -> None:
+    """y = act(LayerNorm(x)) per row of [rows, cols], keeping mean and rstd (float32 [rows])."""
+    _require(x.dim() == 2, "layernorm: x is not [rows, cols]")
+    rows, cols = x.shape
+    _on_current_device("layernorm", x, y, gamma, beta, mean, rstd)
+    _norm_vectors(cols, rows, (gamma, beta), (mean, rstd))
+    _check(lib().w2v_op_layernorm_fwd(_ptr(x), _type_code(x.dtype), _norm_rows("x", x, rows, cols), _ptr(y),
+                                      _type_code(y.dtype), _norm_rows("y", y, rows, cols), rows, cols, _ptr(gamma),
+                                      _ptr(beta), float(eps), int(act), _ptr(mean), _ptr(rstd), _stream(stream)),
+           None, "w2v_op_layernorm_fwd")
+
+
+def w2v_op_layernorm_bwd_workspace(rows: int, cols: int) -> int:
+    return lib().w2v_op_layernorm_bwd_workspace(int(rows), int(cols))
+
+
+def w2v_op_layernorm_bwd(dy, x, gamma, beta, mean, rstd, act: int, dres, dx, dgamma, dbeta, ws=None,
+                         stream=None) -> None:
+    """dx (with dres added, if not None), dgamma and dbeta of w2v_op_layernorm_fwd."""
+    _require(x.dim() == 2, "layernorm: x is not [rows, cols]")
+    rows, cols = x.shape
+    _on_current_device("layernorm", dy, x, gamma, beta, mean, rstd, dx, dgamma, dbeta, *([] if dres is None else [dres]))
+    _norm_vectors(cols, rows, (gamma, beta, dgamma, dbeta), (mean, rstd))
+    _require(dx.dtype == x.dtype and (dres is None or dres.dtype == x.dtype), "layernorm: dx or dres is not of x's type")
+    ws, nbytes = _workspace(ws, w2v_op_layernorm_bwd_workspace(rows, cols), x.device, stream)
+    _check(lib().w2v_op_layernorm_bwd(_ptr(dy), _type_code(dy.dtype), _norm_rows("dy", dy, rows, cols), _ptr(x),
+                                      _type_code(x.dtype), _norm_rows("x", x, rows, cols), rows, cols, _ptr(gamma),
+                                      _ptr(beta), _ptr(mean), _ptr(rstd), int(act), _ptr(dres),
+                                      0 if dres is None else _norm_rows("dres", dres, rows, cols), _ptr(dx),
+                                      _norm_rows("dx", dx, rows, cols), _ptr(dgamma), _ptr(dbeta), _ptr(ws), nbytes,
+                                      _stream(stream)), None, "w2v_op_layernorm_bwd")
+
+
+def w2v_op_grad_clip_workspace(n: int) -> int:
+    return lib().w2v_op_grad_clip_workspace(int(n))
+
+
+def w2v_op_grad_clip(grads, outs, scale: float, max_norm: float, norm, ws=None, stream=None) -> None:
+    """norm[0] = scale * 2-norm of all grads; outs[i] = grads[i] * scale * min(1, max_norm / (norm + 1e-6)).
+    grads, outs: lists of contiguous tensors (outs[i] may be grads[i]); norm: float32 [1] on the device."""
+    import torch
+    n = len(grads)
+    _require(len(outs) == n, "grad_clip: as many outputs as gradients")
+    _on_current_device("grad_clip", norm, *grads, *outs)
+    _require(norm.dtype == torch.float32 and norm.numel() >= 1, "grad_clip: norm is not float32")
+    _require(all(o.dtype == g.dtype and o.numel() == g.numel() and o.is_contiguous() and g.is_contiguous()
+                 for g, o in zip(grads, outs)), "grad_clip: outputs are not contiguous, or not like their gradients")
+    src, dst = (VP * n)(*[g.data_ptr() for g in grads]), (VP * n)(*[o.data_ptr() for o in outs])
+    counts, types = (I64 * n)(*[g.numel() for g in grads]), (I * n)(*[_type_code(g.dtype) for g in grads])
+    ws, nbytes = _workspace(ws, w2v_op_grad_clip_workspace(n), norm.device, stream)
+    _check(lib().w2v_op_grad_clip(n, src, dst, counts, types, float(scale), float(max_norm), _ptr(norm), _ptr(ws),
+                                  nbytes, _stream(stream)), None, "w2v_op_grad_clip")
 
 
 class Model:
