@@ -6,6 +6,7 @@ of falling back to anything else.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional
@@ -124,7 +125,8 @@ def _ptr(x) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without building its Python object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -356,33 +358,41 @@ def w2v_op_wait_probe(err, limit_ns: int, stream=None) -> int:
 
 # ------------------------------------------------------ operators for training
 # (include/w2v_train.h).  Tensors are checked here, since a shape or a device
-# cannot be seen from a pointer; errors raise W2VError.
+# cannot be seen from a pointer; errors raise W2VError.  The checks are written
+# for few interpreter steps: on short clips they take longer than the kernels.
 
 
-def _require(cond: bool, what: str):
-    if not cond:
-        raise W2VError(W2V_EINVAL, what)
+def _refuse(what: str):
+    raise W2VError(W2V_EINVAL, what)
 
 
 def _type_code(dtype) -> int:
     import torch
-    code = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}.get(dtype)
-    _require(code is not None, f"element type {dtype}")
-    return code
+    if dtype == torch.float16:
+        return 0
+    if dtype == torch.bfloat16:
+        return 1
+    if dtype != torch.float32:
+        _refuse(f"element type {dtype}")
+    return 2
 
 
-def _on_current_device(what: str, *tensors):
+def _on_current_device(what: str, tensors):
     import torch
-    _require(all(t.is_cuda for t in tensors), f"{what}: a tensor is not on the GPU")
+    if not all(t.is_cuda for t in tensors):
+        _refuse(f"{what}: a tensor is not on the GPU")
     cur = torch.cuda.current_device()
-    _require(all(t.get_device() == cur for t in tensors), f"{what}: a tensor is not on the current device")
+    for t in tensors:
+        if t.get_device() != cur:
+            _refuse(f"{what}: a tensor is not on the current device")
 
 
 def _workspace(ws, nbytes: int, device, stream):
     """The caller's workspace, or one from torch's allocator, owned by the stream that the call runs on."""
     import torch
     if ws is not None:
-        _require(ws.is_contiguous() and ws.device == device, "workspace: not contiguous, or on another device")
+        if not ws.is_contiguous() or ws.device != device:
+            _refuse("workspace: not contiguous, or on another device")
         return ws, ws.numel() * ws.element_size()
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
@@ -390,37 +400,42 @@ def _workspace(ws, nbytes: int, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
 
 
-def _row_strides(what: str, *tensors):
+def _row_strides(what: str, shape, tensors):
     """(row, clip) strides shared by [batch, T, H*64] tensors whose last axis is contiguous."""
-    batch, T, width = tensors[0].shape
-    strides = None
-    for t in tensors:
-        _require(t.shape == tensors[0].shape and t.dtype == tensors[0].dtype, f"{what}: shapes or types differ")
-        _require(t.stride(2) == 1, f"{what}: the last axis is not contiguous")
-        ld = width if T == 1 else t.stride(1)
-        bs = T * max(ld, width) if batch == 1 else t.stride(0)
-        _require(strides in (None, (ld, bs)), f"{what}: strides differ")
-        strides = (ld, bs)
-    return strides
+    first = tensors[0].stride()
+    if first[2] != 1:
+        _refuse(f"{what}: the last axis is not contiguous")
+    for t in tensors[1:]:
+        st = t.stride()
+        # the stride of an axis with one entry says nothing
+        if st != first and (st[2] != 1 or (shape[1] > 1 and st[1] != first[1]) or (shape[0] > 1 and st[0] != first[0])):
+            _refuse(f"{what}: strides differ")
+    return first[1], first[0]
 
 
 def _attention_shape(qkv, outs, grads, lse, err, frames) -> w2v_attention_shape:
-    q = qkv[0]
-    _require(q.dim() == 3 and q.shape[2] > 0 and q.shape[2] % 64 == 0, "attention: q is not [batch, T, H * 64]")
     import torch
-    batch, T, width = q.shape
-    _on_current_device("attention", *qkv, *outs, *grads, lse, err, *([] if frames is None else [frames]))
-    _require(all(t.shape == q.shape and t.dtype == q.dtype for t in (*qkv, *outs, *grads)),
-             "attention: shapes or types differ")
-    _require(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (batch, width // 64, T),
-             "attention: lse is not a contiguous float32 [batch, H, T]")
-    _require(err.dtype == torch.int32 and err.numel() >= 1, "attention: err is not int32")
-    if frames is not None:
-        _require(frames.dtype == torch.int32 and frames.is_contiguous() and tuple(frames.shape) == (batch,),
-                 "attention: frames is not a contiguous int32 [batch]")
-    return w2v_attention_shape(_type_code(q.dtype), batch, T, width // 64, *_row_strides("attention q, k, v", *qkv),
-                               *_row_strides("attention out", *outs),
-                               *(_row_strides("attention gradients", *grads) if grads else (0, 0)), _ptr(frames))
+    q = qkv[0]
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or shape[2] == 0 or shape[2] % 64:
+        _refuse("attention: q is not [batch, T, H * 64]")
+    batch, T, width = shape
+    rows = qkv + outs + grads
+    _on_current_device("attention", rows + ((lse, err) if frames is None else (lse, err, frames)))
+    for t in rows:
+        if t.dtype != dtype or t.shape != shape:
+            _refuse("attention: shapes or types differ")
+    if lse.dtype != torch.float32 or lse.shape != (batch, width // 64, T) or not lse.is_contiguous():
+        _refuse("attention: lse is not a contiguous float32 [batch, H, T]")
+    if err.dtype != torch.int32 or err.numel() < 1:
+        _refuse("attention: err is not int32")
+    if frames is not None and (frames.dtype != torch.int32 or frames.shape != (batch,) or not frames.is_contiguous()):
+        _refuse("attention: frames is not a contiguous int32 [batch]")
+    return w2v_attention_shape(_type_code(dtype), batch, T, width // 64,
+                               *_row_strides("attention q, k, v", shape, qkv),
+                               *_row_strides("attention out", shape, outs),
+                               *(_row_strides("attention gradients", shape, grads) if grads else (0, 0)),
+                               None if frames is None else frames.data_ptr())
 
 
 def w2v_op_attention_fwd(q, k, v, out, lse, err, frames=None, stream=None) -> None:
@@ -428,12 +443,12 @@ def w2v_op_attention_fwd(q, k, v, out, lse, err, frames=None, stream=None) -> No
     q, k, v (of equal strides), out: fp16 or bf16 [batch, T, H*64]; lse float32
     [batch, H, T]; frames int32 [batch] or None (see include/w2v_train.h)."""
     s = _attention_shape((q, k, v), (out,), (), lse, err, frames)
-    _check(lib().w2v_op_attention_fwd(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(err),
-                                      _stream(stream)), None, "w2v_op_attention_fwd")
+    _check(lib().w2v_op_attention_fwd(s, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                      err.data_ptr(), _stream(stream)), None, "w2v_op_attention_fwd")
 
 
 def w2v_op_attention_bwd_workspace(batch: int, T: int, H: int) -> int:
-    return lib().w2v_op_attention_bwd_workspace(int(batch), int(T), int(H))
+    return lib().w2v_op_attention_bwd_workspace(batch, T, H)
 
 
 def w2v_op_attention_bwd(dout, q, k, v, out, lse, dq, dk, dv, err, frames=None, ws=None, stream=None) -> None:
@@ -442,76 +457,102 @@ def w2v_op_attention_bwd(dout, q, k, v, out, lse, dq, dk, dv, err, frames=None, 
     w2v_op_attention_bwd_workspace bytes, or None for one from torch's allocator."""
     s = _attention_shape((q, k, v), (out, dout), (dq, dk, dv), lse, err, frames)
     ws, nbytes = _workspace(ws, w2v_op_attention_bwd_workspace(s.batch, s.T, s.H), q.device, stream)
-    _check(lib().w2v_op_attention_bwd(ctypes.byref(s), _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                                      _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), nbytes, _ptr(err), _stream(stream)),
-           None, "w2v_op_attention_bwd")
+    _check(lib().w2v_op_attention_bwd(s, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                      lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
+                                      nbytes, err.data_ptr(), _stream(stream)), None, "w2v_op_attention_bwd")
 
 
-def _norm_rows(what: str, t, rows: int, cols: int) -> int:
+def _norm_rows(what: str, t, shape) -> int:
     """Row stride of a [rows, cols] tensor whose last axis is contiguous."""
-    _require(tuple(t.shape) == (rows, cols) and (cols == 1 or t.stride(1) == 1), f"layernorm: {what} is not [rows, cols]")
-    return cols if rows <= 1 else t.stride(0)
+    if t.shape != shape:
+        _refuse(f"layernorm: {what} is not of x's shape")
+    st = t.stride()
+    if st[1] != 1 and shape[1] > 1:
+        _refuse(f"layernorm: {what}'s rows are not contiguous")
+    return shape[1] if shape[0] <= 1 else st[0]
 
 
-def _norm_vectors(cols: int, rows: int, per_col, per_row):
+def _norm_vectors(n: int, vectors):
     import torch
-    for t, n in [(t, cols) for t in per_col] + [(t, rows) for t in per_row]:
-        _require(t.dtype == torch.float32 and t.is_contiguous() and t.numel() == n,
-                 "layernorm: a vector is not contiguous float32 of its size")
+    for t in vectors:
+        if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+            _refuse("layernorm: a vector is not contiguous float32 of its size")
 
 
 def w2v_op_layernorm_fwd(x, y, gamma, beta, eps: float, act: int, mean, rstd, stream=None) -> None:
     """y = act(LayerNorm(x)) per row of [rows, cols], keeping mean and rstd (float32 [rows])."""
-    _require(x.dim() == 2, "layernorm: x is not [rows, cols]")
-    rows, cols = x.shape
-    _on_current_device("layernorm", x, y, gamma, beta, mean, rstd)
-    _norm_vectors(cols, rows, (gamma, beta), (mean, rstd))
-    _check(lib().w2v_op_layernorm_fwd(_ptr(x), _type_code(x.dtype), _norm_rows("x", x, rows, cols), _ptr(y),
-                                      _type_code(y.dtype), _norm_rows("y", y, rows, cols), rows, cols, _ptr(gamma),
-                                      _ptr(beta), float(eps), int(act), _ptr(mean), _ptr(rstd), _stream(stream)),
+    shape = x.shape
+    if len(shape) != 2:
+        _refuse("layernorm: x is not [rows, cols]")
+    rows, cols = shape
+    _on_current_device("layernorm", (x, y, gamma, beta, mean, rstd))
+    _norm_vectors(cols, (gamma, beta))
+    _norm_vectors(rows, (mean, rstd))
+    _check(lib().w2v_op_layernorm_fwd(x.data_ptr(), _type_code(x.dtype), _norm_rows("x", x, shape), y.data_ptr(),
+                                      _type_code(y.dtype), _norm_rows("y", y, shape), rows, cols, gamma.data_ptr(),
+                                      beta.data_ptr(), eps, act, mean.data_ptr(), rstd.data_ptr(), _stream(stream)),
            None, "w2v_op_layernorm_fwd")
 
 
 def w2v_op_layernorm_bwd_workspace(rows: int, cols: int) -> int:
-    return lib().w2v_op_layernorm_bwd_workspace(int(rows), int(cols))
+    return lib().w2v_op_layernorm_bwd_workspace(rows, cols)
 
 
 def w2v_op_layernorm_bwd(dy, x, gamma, beta, mean, rstd, act: int, dres, dx, dgamma, dbeta, ws=None,
                          stream=None) -> None:
-    """dx (with dres added, if not None), dgamma and dbeta of w2v_op_layernorm_fwd."""
-    _require(x.dim() == 2, "layernorm: x is not [rows, cols]")
-    rows, cols = x.shape
-    _on_current_device("layernorm", dy, x, gamma, beta, mean, rstd, dx, dgamma, dbeta, *([] if dres is None else [dres]))
-    _norm_vectors(cols, rows, (gamma, beta, dgamma, dbeta), (mean, rstd))
-    _require(dx.dtype == x.dtype and (dres is None or dres.dtype == x.dtype), "layernorm: dx or dres is not of x's type")
+    """dx (with dres added, if not None), dgamma and dbeta of w2v_op_layernorm_fwd.
+    ws: a workspace of w2v_op_layernorm_bwd_workspace bytes, or None for one from
+    torch's allocator."""
+    shape = x.shape
+    if len(shape) != 2:
+        _refuse("layernorm: x is not [rows, cols]")
+    rows, cols = shape
+    tensors = (dy, x, gamma, beta, mean, rstd, dx, dgamma, dbeta)
+    _on_current_device("layernorm", tensors if dres is None else tensors + (dres,))
+    _norm_vectors(cols, (gamma, beta, dgamma, dbeta))
+    _norm_vectors(rows, (mean, rstd))
+    if dx.dtype != x.dtype or (dres is not None and dres.dtype != x.dtype):
+        _refuse("layernorm: dx or dres is not of x's type")
     ws, nbytes = _workspace(ws, w2v_op_layernorm_bwd_workspace(rows, cols), x.device, stream)
-    _check(lib().w2v_op_layernorm_bwd(_ptr(dy), _type_code(dy.dtype), _norm_rows("dy", dy, rows, cols), _ptr(x),
-                                      _type_code(x.dtype), _norm_rows("x", x, rows, cols), rows, cols, _ptr(gamma),
-                                      _ptr(beta), _ptr(mean), _ptr(rstd), int(act), _ptr(dres),
-                                      0 if dres is None else _norm_rows("dres", dres, rows, cols), _ptr(dx),
-                                      _norm_rows("dx", dx, rows, cols), _ptr(dgamma), _ptr(dbeta), _ptr(ws), nbytes,
-                                      _stream(stream)), None, "w2v_op_layernorm_bwd")
+    _check(lib().w2v_op_layernorm_bwd(dy.data_ptr(), _type_code(dy.dtype), _norm_rows("dy", dy, shape), x.data_ptr(),
+                                      _type_code(x.dtype), _norm_rows("x", x, shape), rows, cols, gamma.data_ptr(),
+                                      beta.data_ptr(), mean.data_ptr(), rstd.data_ptr(), act,
+                                      None if dres is None else dres.data_ptr(),
+                                      0 if dres is None else _norm_rows("dres", dres, shape), dx.data_ptr(),
+                                      _norm_rows("dx", dx, shape), dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(),
+                                      nbytes, _stream(stream)), None, "w2v_op_layernorm_bwd")
 
 
 def w2v_op_grad_clip_workspace(n: int) -> int:
-    return lib().w2v_op_grad_clip_workspace(int(n))
+    return lib().w2v_op_grad_clip_workspace(n)
 
 
 def w2v_op_grad_clip(grads, outs, scale: float, max_norm: float, norm, ws=None, stream=None) -> None:
     """norm[0] = scale * 2-norm of all grads; outs[i] = grads[i] * scale * min(1, max_norm / (norm + 1e-6)).
-    grads, outs: lists of contiguous tensors (outs[i] may be grads[i]); norm: float32 [1] on the device."""
+    grads, outs: lists of contiguous tensors (outs[i] may be grads[i]); norm: float32 [1] on the device.
+    ws: a workspace of w2v_op_grad_clip_workspace bytes, or None for one from torch's allocator."""
     import torch
-    n = len(grads)
-    _require(len(outs) == n, "grad_clip: as many outputs as gradients")
-    _on_current_device("grad_clip", norm, *grads, *outs)
-    _require(norm.dtype == torch.float32 and norm.numel() >= 1, "grad_clip: norm is not float32")
-    _require(all(o.dtype == g.dtype and o.numel() == g.numel() and o.is_contiguous() and g.is_contiguous()
-                 for g, o in zip(grads, outs)), "grad_clip: outputs are not contiguous, or not like their gradients")
-    src, dst = (VP * n)(*[g.data_ptr() for g in grads]), (VP * n)(*[o.data_ptr() for o in outs])
-    counts, types = (I64 * n)(*[g.numel() for g in grads]), (I * n)(*[_type_code(g.dtype) for g in grads])
+    Tensor, n = torch.Tensor, len(grads)
+    if len(outs) != n:
+        _refuse("grad_clip: not as many outputs as gradients")
+    _on_current_device("grad_clip", (norm,))
+    if norm.dtype != torch.float32 or norm.numel() < 1:
+        _refuse("grad_clip: norm is not float32")
+    types, counts = [t.dtype for t in grads], array.array("q", map(Tensor.numel, grads))
+    devices = set(map(Tensor.get_device, grads))
+    devices.update(map(Tensor.get_device, outs))
+    if devices - {norm.get_device()}:
+        _refuse("grad_clip: a tensor is not on the current device")
+    if types != [t.dtype for t in outs] or counts != array.array("q", map(Tensor.numel, outs)) or not (
+            all(map(Tensor.is_contiguous, grads)) and all(map(Tensor.is_contiguous, outs))):
+        _refuse("grad_clip: outputs are not contiguous, or not like their gradients")
+    code = {t: _type_code(t) for t in set(types)}
+    types = array.array("i", [code[t] for t in types])
+    src, dst = array.array("Q", map(Tensor.data_ptr, grads)), array.array("Q", map(Tensor.data_ptr, outs))
     ws, nbytes = _workspace(ws, w2v_op_grad_clip_workspace(n), norm.device, stream)
-    _check(lib().w2v_op_grad_clip(n, src, dst, counts, types, float(scale), float(max_norm), _ptr(norm), _ptr(ws),
-                                  nbytes, _stream(stream)), None, "w2v_op_grad_clip")
+    _check(lib().w2v_op_grad_clip(n, src.buffer_info()[0], dst.buffer_info()[0], counts.buffer_info()[0],
+                                  types.buffer_info()[0], scale, max_norm, norm.data_ptr(), ws.data_ptr(), nbytes,
+                                  _stream(stream)), None, "w2v_op_grad_clip")
 
 
 class Model:
