@@ -51,6 +51,18 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
+// One lane of the (converged) warp.  With the whole warp around the loop and the
+// issue behind this predicate, addresses and descriptors stay in uniform
+// registers; behind `lane == 0` each product took about 90 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// A value that is the same in every lane, in a form that the compiler knows to be.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 __device__ __forceinline__ int clip_frames(const int32_t* frames, int b, int T) {
   if (!frames) return T;
   const int n = frames[b];
@@ -113,7 +125,7 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   uint64_t* kv_empty = bars + 4 + FwdSmem::kStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 + 2 * FwdSmem::kStages);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int qt = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int b = bh / H, h = bh % H;
 
@@ -136,7 +148,7 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   const uint32_t tS = tmem, tO = tmem + 64;
   pdl_wait();
   const int len = clip_frames(frames, b, T);
@@ -187,16 +199,17 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       }
       __syncwarp();
       const uint64_t dK = desc_sw128(smem_u32(kv)), dV = desc_sw128(smem_u32(kv + kTileBytes));
-      if (lane == 0) {
-        tc_fence_after();
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) umma_f16(tS, dQ + 2 * kk, dK + 2 * kk, idS, kk);
         umma_commit(s_full);
       }
+      __syncwarp();
       ok = __all_sync(0xffffffffu, mbar_wait(p_full, j & 1));
       if (!ok) break;
-      if (lane == 0) {
-        tc_fence_after();
+      tc_fence_after();
+      if (elect_one()) {
         // 16 keys a step: 8 packed columns of P, 16 rows (2048 bytes) of V.
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
@@ -456,12 +469,13 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
   uint64_t* dp_full = bars + 2;
   uint64_t* p_full = bars + 3;
   uint64_t* ds_full = bars + 4;
-  uint64_t* acc_done = bars + 5;
-  uint64_t* b_full = bars + 6;
-  uint64_t* b_empty = bars + 6 + BwdSmem::kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6 + 2 * BwdSmem::kStages);
+  uint64_t* v_done = bars + 5;
+  uint64_t* acc_done = bars + 6;
+  uint64_t* b_full = bars + 7;
+  uint64_t* b_empty = bars + 7 + BwdSmem::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 7 + 2 * BwdSmem::kStages);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int b = bh / a.H, h = bh % a.H;
 
   if (threadIdx.x == 0) {
@@ -470,6 +484,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
     mbar_init(dp_full, 1);
     mbar_init(p_full, 8);
     mbar_init(ds_full, 8);
+    mbar_init(v_done, 1);
     mbar_init(acc_done, 1);
     for (int i = 0; i < BwdSmem::kStages; ++i) {
       mbar_init(&b_full[i], 1);
@@ -485,7 +500,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   // Key CTA: dV | dK | S, P | dP, dS.  Query CTA: Q, dO (packed) | dQ | S | dP, dS.
   const uint32_t tAcc1 = tmem, tAcc2 = tmem + 64, tS = tmem + 128, tD = tmem + 192;
   const uint32_t tA1 = tmem, tA2 = tmem + 32;
@@ -534,68 +549,75 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
     constexpr uint32_t idG = idesc_train<BF16>(128, kHd, true);
     const uint64_t dA1 = desc_sw128(smem_u32(smem + BwdSmem::A));
     const uint64_t dA2 = desc_sw128(smem_u32(smem + BwdSmem::A + 2 * kTileBytes));
-    bool ok = n_sub == 0 || __all_sync(0xffffffffu, mbar_wait(a_full, 0));
-    for (int j = 0; ok && j < n_sub; ++j) {
+    const uint64_t dB = desc_sw128(smem_u32(smem + BwdSmem::B));
+    auto tile_b1 = [&](int j) { return dB + static_cast<uint64_t>((j % BwdSmem::kStages) * (2 * kTileBytes >> 4)); };
+    auto tile_b2 = [&](int j) { return tile_b1(j) + (kTileBytes >> 4); };
+    auto wait_tile = [&](int j) {
       const int st = j % BwdSmem::kStages;
-      uint8_t* bt = smem + BwdSmem::B + st * 2 * kTileBytes;
-      // P and dS of the previous tile lie over S and dP: their products must be done.
-      ok = __all_sync(0xffffffffu, mbar_wait(&b_full[st], (j / BwdSmem::kStages) & 1) &&
-                                       (j == 0 || mbar_wait(acc_done, (j - 1) & 1)));
-      if (!ok) break;
+      const bool there = __all_sync(0xffffffffu, mbar_wait(&b_full[st], (j / BwdSmem::kStages) & 1));
       const int valid = len - j * kSub;
-      if (valid < kSub) {
+      if (there && valid < kSub) {
+        uint8_t* bt = smem + BwdSmem::B + st * 2 * kTileBytes;
         zero_tail_rows(bt, valid, lane);
         zero_tail_rows(bt + kTileBytes, valid, lane);
         fence_proxy_async_smem();
-      }
-      __syncwarp();
-      const uint64_t dB1 = desc_sw128(smem_u32(bt)), dB2 = desc_sw128(smem_u32(bt + kTileBytes));
-      if (lane == 0) {
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (KEYS)
-            umma_f16(tS, dA1 + 2 * kk, dB1 + 2 * kk, idS, kk);
-          else
-            umma_f16_ts(tS, tA1 + 8 * kk, dB1 + 2 * kk, idS, kk);
-        }
-        umma_commit(s_full);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (KEYS)
-            umma_f16(tD, dA2 + 2 * kk, dB2 + 2 * kk, idS, kk);
-          else
-            umma_f16_ts(tD, tA2 + 8 * kk, dB2 + 2 * kk, idS, kk);
-        }
-        umma_commit(dp_full);
-      }
-      // P and dS: columns 32 w .. 32 w + 31 packed at columns 32 w .. 32 w + 15,
-      // so the four 16-row steps start at 0, 8, 32 and 40; each is 16 rows (2048
-      // bytes) of the streamed tile.
-      if (KEYS) {
-        ok = __all_sync(0xffffffffu, mbar_wait(p_full, j & 1));
-        if (!ok) break;
-        if (lane == 0) {
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_f16_ts(tAcc1, tS + 32 * (kk >> 1) + 8 * (kk & 1), dB2 + static_cast<uint64_t>(128 * kk), idG,
-                        (j > 0 || kk > 0) ? 1u : 0u);
-        }
         __syncwarp();
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(ds_full, j & 1));
-      if (!ok) break;
-      if (lane == 0) {
-        tc_fence_after();
+      return there;
+    };
+    auto scores = [&](uint32_t d, uint64_t da, uint32_t ta, uint64_t db, uint64_t* bar) {
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_f16_ts(tAcc2, tD + 32 * (kk >> 1) + 8 * (kk & 1), dB1 + static_cast<uint64_t>(128 * kk), idG,
-                      (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&b_empty[st]);
-        umma_commit(acc_done);
+        for (int kk = 0; kk < 4; ++kk) {
+          if (KEYS)
+            umma_f16(d, da + 2 * kk, db + 2 * kk, idS, kk);
+          else
+            umma_f16_ts(d, ta + 8 * kk, db + 2 * kk, idS, kk);
+        }
+        umma_commit(bar);
       }
       __syncwarp();
+    };
+    // P and dS: columns 32 w .. 32 w + 31 packed at columns 32 w .. 32 w + 15, so
+    // the four 16-row steps start at 0, 8, 32 and 40; each is 16 rows (2048 bytes)
+    // of the streamed tile.
+    auto accumulate = [&](uint32_t d, uint32_t ta, uint64_t db, int j, uint64_t* bar, uint64_t* empty) {
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16_ts(d, ta + 32 * (kk >> 1) + 8 * (kk & 1), db + static_cast<uint64_t>(128 * kk), idG,
+                      (j > 0 || kk > 0) ? 1u : 0u);
+        if (empty) umma_commit(empty);
+        umma_commit(bar);
+      }
+      __syncwarp();
+    };
+    auto wait = [&](uint64_t* bar, int j) { return __all_sync(0xffffffffu, mbar_wait(bar, j & 1)); };
+    bool ok = n_sub == 0 || (__all_sync(0xffffffffu, mbar_wait(a_full, 0)) && wait_tile(0));
+    if (ok && n_sub > 0) {
+      scores(tS, dA1, tA1, tile_b1(0), s_full);
+      scores(tD, dA2, tA2, tile_b2(0), dp_full);
+    }
+    // The next tile's scores run while the warps form this tile's dS, and its dP
+    // while they form the next P, each as soon as its columns are free: those of S
+    // once P's product is done (key CTA) or S has been read (query CTA), those of
+    // dP once dS's product is done.
+    for (int j = 0; ok && j < n_sub; ++j) {
+      const bool more = j + 1 < n_sub;
+      if (!(ok = wait(p_full, j))) break;
+      if (KEYS) accumulate(tAcc1, tS, tile_b2(j), j, v_done, nullptr);
+      if (more) {
+        if (!(ok = wait_tile(j + 1) && (!KEYS || wait(v_done, j)))) break;
+        scores(tS, dA1, tA1, tile_b1(j + 1), s_full);
+      }
+      if (!(ok = wait(ds_full, j))) break;
+      accumulate(tAcc2, tD, tile_b1(j), j, acc_done, &b_empty[j % BwdSmem::kStages]);
+      if (more) {
+        if (!(ok = wait(acc_done, j))) break;
+        scores(tD, dA2, tA2, tile_b2(j + 1), dp_full);
+      }
     }
     if (!ok && lane == 0) atomicOr(a.err, kErrWaitMma);
   } else {
@@ -631,13 +653,21 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
       const int valid = len - j * kSub - half * 32;
       float s[32];
       uint32_t pk[16];
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, j & 1));
-      // the statistics came with the streamed tile, whose arrival only the
-      // product warp has seen
-      if (KEYS && ok) ok = __all_sync(0xffffffffu, mbar_wait(&b_full[j % BwdSmem::kStages], (j / BwdSmem::kStages) & 1));
+      // (KEYS: the statistics came with the streamed tile, whose arrival only the
+      // product warp has seen)
+      if (ok)
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full, j & 1) &&
+                                         (!KEYS || mbar_wait(&b_full[j % BwdSmem::kStages], (j / BwdSmem::kStages) & 1)));
       if (ok) {
         tc_fence_after();
         tmem_ld32(tS + lane_base + half * 32, s);
+      }
+      if (!KEYS) {  // S has been read: its columns are free for the next tile's
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+      }
+      if (ok) {
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
           float4 l4 = make_float4(row_l, row_l, row_l, row_l);
