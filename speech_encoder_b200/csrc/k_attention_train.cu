@@ -69,6 +69,61 @@ __device__ __forceinline__ int clip_frames(const int32_t* frames, int b, int T) 
   return n < 0 ? 0 : (n > T ? T : n);
 }
 
+// The clip with the rank-th most frames (ties by index), for batches small enough
+// that every CTA can afford to look: work is handed out in grid order, so with the
+// longest clips first the last CTAs to start are short ones.  All lanes of the
+// warp take part and get the same answer.
+constexpr int kRankedBatch = 64;
+__device__ __forceinline__ int clip_of_rank(const int32_t* frames, int batch, int T, int rank, int lane) {
+  if (batch > kRankedBatch) return rank;
+  for (int base = 0; base < batch; base += 32) {
+    const int c = base + lane;
+    const int n = c < batch ? clip_frames(frames, c, T) : -1;
+    int r = 0;
+    for (int o = 0; o < batch; ++o) {
+      const int m = clip_frames(frames, o, T);
+      r += m > n || (m == n && o < c);
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, c < batch && r == rank);
+    if (hit) return base + __ffs(hit) - 1;
+  }
+  return 0;
+}
+
+// 2^x of a pair on the FMA and ALU pipes, for the share of the exponentials that
+// the exponent unit (16 a clock per SM) has no time for: x = j + f with j the
+// nearest integer (adding 1.5 * 2^23 leaves j in the low mantissa bits), 2^f by the
+// polynomial of degree 4 with the smallest largest relative error on [-1/2, 1/2]
+// (2.7e-6, found by linear programming over a fine grid), j added to the
+// exponent.  x is clamped below at -126.
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+  constexpr float kMagic = 12582912.0f;
+  x = make_float2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
+  const float2 t = fadd2(x, make_float2(kMagic, kMagic));
+  const float2 j = fadd2(t, make_float2(-kMagic, -kMagic));
+  const float2 f = ffma2(j, make_float2(-1.0f, -1.0f), x);
+  float2 p = ffma2(f, make_float2(0.009567738510668278f, 0.009567738510668278f),
+                   make_float2(0.05591749772429466f, 0.05591749772429466f));
+  p = ffma2(p, f, make_float2(0.24024811387062073f, 0.24024811387062073f));
+  p = ffma2(p, f, make_float2(0.6931219100952148f, 0.6931219100952148f));
+  p = ffma2(p, f, make_float2(0.9999992251396179f, 0.9999992251396179f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// 2^x of pair number i of a row part; POLY of every 4 pairs by polynomial.
+template <int POLY>
+__device__ __forceinline__ float2 exp2_pair(float2 x, int i) {
+  if ((i & 3) < POLY) return exp2_poly(x);
+  return make_float2(ex2_approx(x.x), ex2_approx(x.y));
+}
+
+// Zeros over the 64 columns of one head in rows [from, to).
+__device__ __forceinline__ void zero_rows(uint16_t* p, int64_t ld, int from, int to) {
+  for (int i = threadIdx.x; i < (to - from) * 8; i += blockDim.x)
+    *reinterpret_cast<uint4*>(p + (from + (i >> 3)) * ld + (i & 7) * 8) = make_uint4(0, 0, 0, 0);
+}
+
 // Zeros rows [valid, 64) of a 64-row tile (one warp).  Zero chunks do not care
 // about the swizzle.
 __device__ __forceinline__ void zero_tail_rows(uint8_t* tile, int valid, int lane) {
@@ -76,21 +131,34 @@ __device__ __forceinline__ void zero_tail_rows(uint8_t* tile, int valid, int lan
     *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// One thread's 32 columns of an accumulator row, scaled and rounded; zeros where
-// the row is not live (the accumulator may then hold anything).
+// Offset of 16-byte chunk c of row r in a tile of 128-byte rows, 128-byte swizzled.
+__device__ __forceinline__ int swizzled(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+// One thread's 32 columns of an accumulator row, scaled and rounded, into a staged
+// tile of 128 rows (chunks c0 .. c0 + 3); zeros where the row is not live (the
+// accumulator may then hold anything).
 template <bool BF16>
-__device__ __forceinline__ void store_row_part(uint32_t taddr, uint16_t* dst, float scale, bool write, bool live) {
+__device__ __forceinline__ void stage_row_part(uint32_t taddr, uint8_t* tile, int r, int c0, float scale, bool live) {
   float v[32];
   tmem_ld32(taddr, v);
-  if (!write) return;
 #pragma unroll
   for (int i = 0; i < 32; i += 8) {
     uint4 u = make_uint4(0, 0, 0, 0);
     if (live)
       u = make_uint4(pack2<BF16>(v[i] * scale, v[i + 1] * scale), pack2<BF16>(v[i + 2] * scale, v[i + 3] * scale),
                      pack2<BF16>(v[i + 4] * scale, v[i + 5] * scale), pack2<BF16>(v[i + 6] * scale, v[i + 7] * scale));
-    *reinterpret_cast<uint4*>(dst + i) = u;
+    *reinterpret_cast<uint4*>(tile + swizzled(r, c0 + i / 8)) = u;
   }
+}
+
+// A staged tile to rows [0, rows) of one head, eight threads a row (a thread per
+// row, straight from its registers, writes 32 lines an instruction and took 2.3 us
+// for two tiles where this takes 0.9).
+__device__ __forceinline__ void store_tile(const uint8_t* tile, uint16_t* dst, int64_t ld, int rows, int tid,
+                                           int threads) {
+  for (int i = tid; i < rows * 8; i += threads)
+    *reinterpret_cast<uint4*>(dst + (i >> 3) * ld + (i & 7) * 8) =
+        *reinterpret_cast<const uint4*>(tile + swizzled(i >> 3, i & 7));
 }
 
 // -------------------------------------------------------------------- forward
@@ -107,12 +175,18 @@ struct FwdSmem {
   static constexpr int TOTAL = BAR + 128 + 1024;
 };
 constexpr int kFwdThreads = 192;
+#ifndef FWD_POLY
+#define FWD_POLY 2
+#endif
+#ifndef BWD_POLY
+#define BWD_POLY 0
+#endif
 
 template <bool BF16>
 __global__ void __launch_bounds__(kFwdThreads, 4)
 attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const int32_t* __restrict__ frames, int T, int H,
-                     int tiles, uint16_t* __restrict__ out, int64_t out_ld, int64_t out_bs, float* __restrict__ lse,
+                     int batch, int tiles, uint16_t* __restrict__ out, int64_t out_ld, int64_t out_bs, float* __restrict__ lse,
                      int* err) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -126,8 +200,22 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 + 2 * FwdSmem::kStages);
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int qt = blockIdx.x % tiles, bh = blockIdx.x / tiles;
-  const int b = bh / H, h = bh % H;
+  const int qt = blockIdx.x % tiles, h = blockIdx.x / tiles % H;
+  int b = blockIdx.x / tiles / H, len = T;
+  if (frames) {
+    pdl_wait();
+    b = clip_of_rank(frames, batch, T, b, lane);
+    len = clip_frames(frames, b, T);
+  }
+  const int64_t bh = static_cast<int64_t>(b) * H + h;
+  const int nkv = (len + kSub - 1) / kSub;
+  if (qt * 128 >= len) {  // rows past the clip
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    const int to = min(T, qt * 128 + 128);
+    zero_rows(out + b * out_bs + h * kHd, out_ld, qt * 128, to);
+    for (int t = qt * 128 + threadIdx.x; t < to; t += kFwdThreads) lse[bh * T + t] = -INFINITY;
+    return;
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -150,12 +238,10 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
   const uint32_t tS = tmem, tO = tmem + 64;
-  pdl_wait();
-  const int len = clip_frames(frames, b, T);
-  const int nkv = qt * 128 < len ? (len + kSub - 1) / kSub : 0;  // no key tile for rows past the clip
+  if (!frames) pdl_wait();
 
   if (warp == 4) {
-    if (lane == 0 && nkv > 0) {
+    if (lane == 0) {
       mbar_arrive_expect_tx(q_full, 2 * kTileBytes);
       tma_load_3d(smem + FwdSmem::Q, &tmQ, q_full, h * kHd, qt * 128, b);
       tma_load_3d(smem + FwdSmem::Q + kTileBytes, &tmQ, q_full, h * kHd, qt * 128 + kSub, b);
@@ -184,7 +270,7 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     constexpr uint32_t idS = idesc_train<BF16>(128, kSub, false);
     constexpr uint32_t idO = idesc_train<BF16>(128, kHd, true);
     const uint64_t dQ = desc_sw128(smem_u32(smem + FwdSmem::Q));
-    bool ok = nkv == 0 || mbar_wait(q_full, 0);
+    bool ok = mbar_wait(q_full, 0);
     for (int j = 0; j < nkv; ++j) {
       const int st = j % FwdSmem::kStages;
       uint8_t* kv = smem + FwdSmem::KV + st * 2 * kTileBytes;
@@ -277,7 +363,7 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             const float2 x = ffma2(make_float2(s[i], s[i + 1]), make_float2(kC2, kC2), make_float2(-m_ref, -m_ref));
-            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            const float2 p = exp2_pair<FWD_POLY>(x, i / 2);
             sum = fadd2(sum, p);
             pk[i / 2] = pack2<BF16>(p.x, p.y);
           }
@@ -289,19 +375,22 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
     }
-    if (nkv > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (nkv - 1) & 1));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (nkv - 1) & 1));
     const int t = qt * 128 + r;
     if (ok) {
       tc_fence_after();
       const bool live = t < len;
       const float inv = live ? 1.0f / l : 0.f;
-      uint16_t* dst = out + b * out_bs + t * out_ld + h * kHd;
 #pragma unroll
-      for (int c0 = 0; c0 < kHd; c0 += 32) store_row_part<BF16>(tO + lane_base + c0, dst + c0, inv, t < T, live);
-      if (t < T) lse[static_cast<int64_t>(bh) * T + t] = live ? m_ref * kLn2 + logf(l) : -INFINITY;
+      for (int c0 = 0; c0 < kHd; c0 += 32)  // over Q, which nothing reads any more
+        stage_row_part<BF16>(tO + lane_base + c0, smem + FwdSmem::Q, r, c0 / 8, inv, live);
+      if (t < T) lse[bh * T + t] = live ? m_ref * kLn2 + logf(l) : -INFINITY;
     } else if (lane == 0) {
       atomicOr(err, kErrWaitSoftmax);
     }
+    named_barrier_sync(1, 128);
+    store_tile(smem + FwdSmem::Q, out + b * out_bs + static_cast<int64_t>(qt) * 128 * out_ld + h * kHd, out_ld,
+               min(128, T - qt * 128), threadIdx.x, 128);
   }
 
   tc_fence_before();
@@ -313,17 +402,76 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 }
 
 // -------------------------------------------------- backward: row statistics
-// Per (clip, head, frame), padded to a multiple of 128 frames:
-//   neg_l = -lse log2(e), -infinity where there is no probability, and
-//   neg_d = -rowsum(dout o out), 0 there;
-// in fp16 also, per 128 frames, the largest |dout row|^2 and |v row|^2.
+// The statistics of a row reach S and dP inside the products: 16 more channels on
+// each side, a row's pieces against constants, make
+//   S = q k^T - 8 lse,   dP = dout v^T - rowsum(dout o out)
+// in the fp32 accumulator.  Without them every thread of a key CTA read two
+// statistics per column from shared memory (16 wide loads and 16 additions per 32
+// columns, a quarter of its time).  A value is split into three pieces of the
+// operand type, hi + mid + lo, each the rounding of what is left: 24 bits in bf16,
+// 33 in fp16.  fp16's range is widened by groups of three channels with different
+// constants c, of which a value uses the first where value / c fits:
+//   lse:    64 (up to 2^21), 2^15
+//   rowsum: 2^-24 (up to 2^-10), 2^-14 (1), 2^-4 (2^10), 2^6 (2^20), 2^15
+// Rows that carry nothing get lse = infinity, so that their probabilities are 0.
+//
+// Layout, per (clip, head): rows padded to a multiple of 128, in the unswizzled
+// K-major core-matrix order [8 rows][2][8][16 bytes], so that any multiple of 8
+// rows is one contiguous operand.
+constexpr int kAugRow = 32;                       // bytes: 16 channels
+constexpr uint32_t kAugLbo = 128, kAugSbo = 256;  // next 8 channels, next 8 rows
+
+__device__ __forceinline__ int aug_offset(int row, int half) { return (row >> 3) * 256 + half * 128 + (row & 7) * 16; }
+
+// The constants of channels 8 half .. 8 half + 7.
+template <bool BF16>
+__device__ __forceinline__ uint4 aug_constants(bool rowsum, int half) {
+  if (BF16) return half ? make_uint4(0, 0, 0, 0) : make_uint4(0x3F803F80u, 0x00003F80u, 0, 0);
+  // fp16 bits: 64 = 5400, 2^15 = 7800, 2^-24 = 0001, 2^-14 = 0400, 2^-4 = 2C00, 2^6 = 5400
+  if (!rowsum) return half ? make_uint4(0, 0, 0, 0) : make_uint4(0x54005400u, 0x78005400u, 0x78007800u, 0);
+  return half ? make_uint4(0x54002C00u, 0x54005400u, 0x78007800u, 0x00007800u)
+              : make_uint4(0x00010001u, 0x04000001u, 0x04000400u, 0x2C002C00u);
+}
+
+// Channels 8 half .. 8 half + 7 of value v (v = -infinity: hi = -infinity).
+template <bool BF16>
+__device__ __forceinline__ uint4 aug_pieces(float v, bool rowsum, int half) {
+  int group = 0;
+  float x = v;
+  if (!BF16) {
+    const float m = fabsf(v);
+    if (rowsum) {
+      group = m <= 0x1p-10f ? 0 : m <= 1.0f ? 1 : m <= 0x1p10f ? 2 : m <= 0x1p20f ? 3 : 4;
+      const float inv = group == 0 ? 0x1p24f : group == 1 ? 0x1p14f : group == 2 ? 0x1p4f : group == 3 ? 0x1p-6f : 0x1p-15f;
+      x = v * inv;
+    } else {
+      group = m <= 0x1p21f || v == -INFINITY ? 0 : 1;
+      x = v * (group == 0 ? 0x1p-6f : 0x1p-15f);
+    }
+  }
+  float r[3];
+  r[0] = unpack2<BF16>(pack2<BF16>(x, 0.f)).x;
+  const float rest = v == -INFINITY ? 0.f : x - r[0];
+  r[1] = unpack2<BF16>(pack2<BF16>(rest, 0.f)).x;
+  r[2] = rest - r[1];
+  float ch[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int piece = half * 8 + i - 3 * group;
+    ch[i] = piece == 0 ? r[0] : piece == 1 ? r[1] : piece == 2 ? r[2] : 0.f;
+  }
+  return make_uint4(pack2<BF16>(ch[0], ch[1]), pack2<BF16>(ch[2], ch[3]), pack2<BF16>(ch[4], ch[5]),
+                    pack2<BF16>(ch[6], ch[7]));
+}
+
+// In fp16 also, per 128 frames, the largest |dout row|^2 and |v row|^2.
 // Eight lanes a row, 16 bytes each.
 template <bool BF16>
 __global__ void __launch_bounds__(256)
 attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ out, int64_t out_ld,
                           int64_t out_bs, const uint16_t* __restrict__ v, int64_t v_ld, int64_t v_bs,
                           const float* __restrict__ lse, const int32_t* __restrict__ frames, int T, int H, int tiles,
-                          float* __restrict__ neg_l, float* __restrict__ neg_d, float2* __restrict__ peak) {
+                          uint8_t* __restrict__ aug_l, uint8_t* __restrict__ aug_d, float2* __restrict__ peak) {
   if (threadIdx.x == 0) pdl_launch_dependents();
   const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int b = bh / H, h = bh % H;
@@ -331,28 +479,35 @@ attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __r
   pdl_wait();
   const int len = clip_frames(frames, b, T);
   float top_do = 0.f, top_v = 0.f;
+  // every load of the thread's four rows before any arithmetic
+  uint4 ra[4], ro[4], rv[4];
+  float rl[4];
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int t = tile * 128 + it * 32 + (threadIdx.x >> 3);
+    ra[it] = ro[it] = rv[it] = make_uint4(0, 0, 0, 0);
+    rl[it] = -INFINITY;
+    if (t < len) {
+      const int64_t at = b * out_bs + t * out_ld + h * kHd + part * 8;
+      ra[it] = *reinterpret_cast<const uint4*>(dout + at);
+      ro[it] = *reinterpret_cast<const uint4*>(out + at);
+      if (!BF16) rv[it] = *reinterpret_cast<const uint4*>(v + b * v_bs + t * v_ld + h * kHd + part * 8);
+      rl[it] = lse[static_cast<int64_t>(bh) * T + t];
+    }
+  }
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
     const int t = tile * 128 + it * 32 + (threadIdx.x >> 3);
     float d = 0.f, ndo = 0.f, nv = 0.f;
-    if (t < len) {
-      const int64_t at = b * out_bs + t * out_ld + h * kHd + part * 8;
-      const uint4 a = *reinterpret_cast<const uint4*>(dout + at), o = *reinterpret_cast<const uint4*>(out + at);
-      const uint32_t au[4] = {a.x, a.y, a.z, a.w}, ou[4] = {o.x, o.y, o.z, o.w};
+    const uint32_t au[4] = {ra[it].x, ra[it].y, ra[it].z, ra[it].w}, ou[4] = {ro[it].x, ro[it].y, ro[it].z, ro[it].w};
+    const uint32_t wu[4] = {rv[it].x, rv[it].y, rv[it].z, rv[it].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 x = unpack2<BF16>(au[i]), y = unpack2<BF16>(ou[i]);
-        d = fmaf(x.x, y.x, fmaf(x.y, y.y, d));
-        if (!BF16) ndo = fmaf(x.x, x.x, fmaf(x.y, x.y, ndo));
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack2<BF16>(au[i]), y = unpack2<BF16>(ou[i]), z = unpack2<BF16>(wu[i]);
+      d = fmaf(x.x, y.x, fmaf(x.y, y.y, d));
       if (!BF16) {
-        const uint4 w = *reinterpret_cast<const uint4*>(v + b * v_bs + t * v_ld + h * kHd + part * 8);
-        const uint32_t wu[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = unpack2<BF16>(wu[i]);
-          nv = fmaf(x.x, x.x, fmaf(x.y, x.y, nv));
-        }
+        ndo = fmaf(x.x, x.x, fmaf(x.y, x.y, ndo));
+        nv = fmaf(z.x, z.x, fmaf(z.y, z.y, nv));
       }
     }
 #pragma unroll
@@ -367,11 +522,12 @@ attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __r
       top_do = fmaxf(top_do, ndo);
       top_v = fmaxf(top_v, nv);
     }
-    if (part == 0) {
-      const int64_t at = static_cast<int64_t>(bh) * tiles * 128 + t;
-      const float l = t < len ? lse[static_cast<int64_t>(bh) * T + t] : -INFINITY;
-      neg_l[at] = l == -INFINITY ? -INFINITY : -l * kLog2e;
-      neg_d[at] = t < len ? -d : 0.f;
+    if (part < 4) {
+      const bool rowsum = part >= 2;
+      const float value = rowsum ? -d : (rl[it] == -INFINITY ? -INFINITY : -8.0f * rl[it]);
+      uint8_t* dst = (rowsum ? aug_d : aug_l) + (static_cast<int64_t>(bh) * tiles + tile) * 128 * kAugRow;
+      *reinterpret_cast<uint4*>(dst + aug_offset(it * 32 + (threadIdx.x >> 3), part & 1)) =
+          aug_pieces<BF16>(value, rowsum, part & 1);
     }
   }
   if (!BF16) {
@@ -393,11 +549,11 @@ attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __r
   }
 }
 
-// Scale of dS in fp16, a power of two: |dS_ij| <= P_ij |dout_i| |v_j - out_i|
+// Exponent of the scale of dS in fp16: |dS_ij| <= P_ij |dout_i| |v_j - out_i|
 // <= 2 max|dout| max|v| (out_i is a mean of v rows), so with that bound brought
 // just under 2^15 no entry overflows and the smallest keep what precision fp16
 // can give them.  Every thread of the warp gets the same value.
-__device__ __forceinline__ float ds_scale(const float2* peak, int tiles, int lane) {
+__device__ __forceinline__ int ds_exponent(const float2* peak, int tiles, int lane) {
   float top_do = 0.f, top_v = 0.f;
   for (int i = lane; i < tiles; i += 32) {
     const float2 p = peak[i];
@@ -410,81 +566,95 @@ __device__ __forceinline__ float ds_scale(const float2* peak, int tiles, int lan
     top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
   }
   const float bound = 2.0f * sqrtf(top_do) * sqrtf(top_v);
-  if (!(bound > 0.f) || !(bound < INFINITY)) return 1.0f;
-  const int e = max(-100, min(100, 14 - ilogbf(bound)));
-  return scalbnf(1.0f, e);
+  if (!(bound > 0.f) || !(bound < INFINITY)) return 0;
+  return max(-100, min(100, 14 - ilogbf(bound)));
 }
 
 // ------------------------------------------------------------------- backward
 // Two kinds of CTA in one launch, with the same inner step.  A CTA holds 128
 // rows of a pair of operands (A1, A2) and streams 64-row tiles of the other
-// pair (B1, B2); per tile
-//   S = A1 B1^T, dP = A2 B2^T             (M = 128, N = 64, K = 64)
-//   P = 2^(S c + neg_l), dS = P o (dP + neg_d)
+// pair (B1, B2), each with its 16 statistics channels; per tile
+//   S = A1 B1^T, dP = A2 B2^T             (M = 128, N = 64, K = 64 + 16)
+//   P = 2^(S c), dS = P o dP
 // A key CTA holds (K, V) and streams (Q, dO); its S, P and dS are transposed
-// (row = key), the statistics belong to columns, and P and dS, rounded to the
-// operand type in tensor memory over S and dP, are the A operands of
+// (row = key) and, rounded to the operand type, the A operands of
 //   dV += P dO, dK += dS Q                 (M = 128, N = 64, K = 64 queries).
-// A query CTA holds (Q, dO), streams (K, V), has one row's statistics per
-// thread, and needs only dQ += dS K.  S and dP are computed twice, which costs
-// 7 products instead of the 5 of a single pass, but each gradient has one owner
-// that sums it in a fixed order: no atomics and no fp32 partial sums in memory.
+// A query CTA holds (Q, dO), streams (K, V) and needs only dQ += dS K.  S and dP
+// are computed twice, which costs 7 products instead of the 5 of a single pass,
+// but each gradient has one owner that sums it in a fixed order: no atomics and no
+// fp32 partial sums in memory.
 //
-// Warps 0-7: one TMEM lane quarter and 32 of the 64 columns each; warp 8 TMA;
-// warp 9 tensor memory and products.  256 tensor-memory columns and 99 KB of
-// shared memory: two CTAs per SM fill each other's gaps.
+// Warps 0-7: one TMEM lane quarter and 32 of the 64 columns each; they pack dS and
+// P together over the dP columns that they have read, so the S columns are free
+// for the next tile as soon as they are read.  Warp 8: TMA; warp 9: tensor memory
+// and products.  256 tensor-memory columns and 100 KB of shared memory: two CTAs
+// per SM fill each other's gaps.
 struct BwdSmem {
-  static constexpr int kStages = 4;
-  static constexpr int A = 0;                      // key CTA: K, V (128 rows each)
+  static constexpr int kStages = 3;
+  static constexpr int A = 0;                      // A1, A2 (128 rows each); at the end the gradients' tiles
   static constexpr int B = 4 * kTileBytes;         // [stages]{B1, B2}
-  static constexpr int STAT = B + kStages * 2 * kTileBytes;  // [stages]{neg_l[64], neg_d[64]}
-  static constexpr int BAR = STAT + kStages * 512;
+  static constexpr int AugA = B + kStages * 2 * kTileBytes;  // {lse, rowsum} channels of A's 128 rows
+  static constexpr int AugB = AugA + 2 * 128 * kAugRow;      // [stages]{lse, rowsum} of the streamed rows
+  static constexpr int kAugTile = kSub * kAugRow;
+  static constexpr int BAR = AugB + kStages * 2 * kAugTile;
   static constexpr int TOTAL = BAR + 256 + 1024;
 };
 constexpr int kBwdThreads = 320;
 
 struct BwdArgs {
-  const uint16_t* q;
-  const uint16_t* dout;
   uint16_t* dq;
   uint16_t* dk;
   uint16_t* dv;
-  int64_t qkv_ld, qkv_bs, out_ld, out_bs, grad_ld, grad_bs;
+  int64_t grad_ld, grad_bs;
   const int32_t* frames;
-  const float* neg_l;
-  const float* neg_d;
+  const uint8_t* aug_l;
+  const uint8_t* aug_d;
   const float2* peak;
-  int T, H, tiles, bh;
+  int T, H, batch, tiles;
   int* err;
 };
 
 template <bool BF16, bool KEYS>
 __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensorMap& tmA2, const CUtensorMap& tmB1,
-                                         const CUtensorMap& tmB2, const BwdArgs& a, int tile, int bh) {
+                                         const CUtensorMap& tmB2, const BwdArgs& a, int unit) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BwdSmem::BAR);
   uint64_t* a_full = bars;
   uint64_t* s_full = bars + 1;
   uint64_t* dp_full = bars + 2;
-  uint64_t* p_full = bars + 3;
+  uint64_t* s_read = bars + 3;
   uint64_t* ds_full = bars + 4;
-  uint64_t* v_done = bars + 5;
-  uint64_t* acc_done = bars + 6;
-  uint64_t* b_full = bars + 7;
-  uint64_t* b_empty = bars + 7 + BwdSmem::kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 7 + 2 * BwdSmem::kStages);
+  uint64_t* acc_done = bars + 5;
+  uint64_t* b_full = bars + 6;
+  uint64_t* b_empty = bars + 6 + BwdSmem::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6 + 2 * BwdSmem::kStages);
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int b = bh / a.H, h = bh % a.H;
+  const int tile = unit % a.tiles, h = unit / a.tiles % a.H;
+  int b = unit / a.tiles / a.H, len = a.T;
+  if (a.frames) {
+    pdl_wait();
+    b = clip_of_rank(a.frames, a.batch, a.T, b, lane);
+    len = clip_frames(a.frames, b, a.T);
+  }
+  const int64_t bh = static_cast<int64_t>(b) * a.H + h;
+  const int n_sub = (len + kSub - 1) / kSub;
+  if (tile * 128 >= len) {  // rows past the clip
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    const int to = min(a.T, tile * 128 + 128);
+    const int64_t at = b * a.grad_bs + h * kHd;
+    zero_rows((KEYS ? a.dk : a.dq) + at, a.grad_ld, tile * 128, to);
+    if (KEYS) zero_rows(a.dv + at, a.grad_ld, tile * 128, to);
+    return;
+  }
 
   if (threadIdx.x == 0) {
-    mbar_init(a_full, KEYS ? 1 : 8);
+    mbar_init(a_full, 1);
+    mbar_init(s_read, 8);
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    mbar_init(p_full, 8);
     mbar_init(ds_full, 8);
-    mbar_init(v_done, 1);
     mbar_init(acc_done, 1);
     for (int i = 0; i < BwdSmem::kStages; ++i) {
       mbar_init(&b_full[i], 1);
@@ -497,28 +667,35 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
     tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
+  // The constants that the other side's pieces meet: A's in a key CTA, one tile of
+  // B's in a query CTA.
+  for (int i = threadIdx.x; i < (KEYS ? 128 : kSub) * 4; i += kBwdThreads) {
+    const int row = i >> 2, half = i & 1, rowsum = (i >> 1) & 1;
+    uint8_t* dst = KEYS ? smem + BwdSmem::AugA + rowsum * 128 * kAugRow : smem + BwdSmem::AugB + rowsum * BwdSmem::kAugTile;
+    *reinterpret_cast<uint4*>(dst + aug_offset(row, half)) = aug_constants<BF16>(rowsum, half);
+  }
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
-  // Key CTA: dV | dK | S, P | dP, dS.  Query CTA: Q, dO (packed) | dQ | S | dP, dS.
+  // dV (key CTA) | dK or dQ | S | dP, then dS and P
   const uint32_t tAcc1 = tmem, tAcc2 = tmem + 64, tS = tmem + 128, tD = tmem + 192;
-  const uint32_t tA1 = tmem, tA2 = tmem + 32;
-  pdl_wait();
-  const int len = clip_frames(a.frames, b, a.T);
-  const int n_sub = tile * 128 < len ? (len + kSub - 1) / kSub : 0;
+  if (!a.frames) pdl_wait();
 
   if (warp == 8) {
-    if (lane == 0 && n_sub > 0) {
-      if (KEYS) {
-        mbar_arrive_expect_tx(a_full, 4 * kTileBytes);
-        for (int i = 0; i < 2; ++i) {
-          tma_load_3d(smem + BwdSmem::A + i * kTileBytes, &tmA1, a_full, h * kHd, tile * 128 + i * kSub, b);
-          tma_load_3d(smem + BwdSmem::A + (2 + i) * kTileBytes, &tmA2, a_full, h * kHd, tile * 128 + i * kSub, b);
-        }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(a_full, 4 * kTileBytes + (KEYS ? 0 : 2 * 128 * kAugRow));
+      for (int i = 0; i < 2; ++i) {
+        tma_load_3d(smem + BwdSmem::A + i * kTileBytes, &tmA1, a_full, h * kHd, tile * 128 + i * kSub, b);
+        tma_load_3d(smem + BwdSmem::A + (2 + i) * kTileBytes, &tmA2, a_full, h * kHd, tile * 128 + i * kSub, b);
       }
-      const float* nl = a.neg_l + static_cast<int64_t>(bh) * a.tiles * 128;
-      const float* nd = a.neg_d + static_cast<int64_t>(bh) * a.tiles * 128;
+      const uint8_t* al = a.aug_l + bh * a.tiles * 128 * kAugRow;
+      const uint8_t* ad = a.aug_d + bh * a.tiles * 128 * kAugRow;
+      if (!KEYS) {
+        bulk_load(smem + BwdSmem::AugA, al + tile * 128 * kAugRow, 128 * kAugRow, a_full);
+        bulk_load(smem + BwdSmem::AugA + 128 * kAugRow, ad + tile * 128 * kAugRow, 128 * kAugRow, a_full);
+      }
       int issued = 0;
       bool ok = true;
       for (int j = 0; j < n_sub; ++j) {
@@ -529,17 +706,18 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
           break;
         }
         uint8_t* dst = smem + BwdSmem::B + st * 2 * kTileBytes;
-        mbar_arrive_expect_tx(&b_full[st], 2 * kTileBytes + (KEYS ? 512 : 0));
+        mbar_arrive_expect_tx(&b_full[st], 2 * kTileBytes + (KEYS ? 2 * BwdSmem::kAugTile : 0));
         tma_load_3d(dst, &tmB1, &b_full[st], h * kHd, j * kSub, b);
         tma_load_3d(dst + kTileBytes, &tmB2, &b_full[st], h * kHd, j * kSub, b);
         if (KEYS) {
-          bulk_load(smem + BwdSmem::STAT + st * 512, nl + j * kSub, 256, &b_full[st]);
-          bulk_load(smem + BwdSmem::STAT + st * 512 + 256, nd + j * kSub, 256, &b_full[st]);
+          uint8_t* aug = smem + BwdSmem::AugB + st * 2 * BwdSmem::kAugTile;
+          bulk_load(aug, al + j * BwdSmem::kAugTile, BwdSmem::kAugTile, &b_full[st]);
+          bulk_load(aug + BwdSmem::kAugTile, ad + j * BwdSmem::kAugTile, BwdSmem::kAugTile, &b_full[st]);
         }
         issued = j + 1;
       }
       if (!ok) {  // wait for the copies in flight before the CTA's shared memory goes
-        if (KEYS) mbar_wait(a_full, 0);
+        mbar_wait(a_full, 0);
         for (int j = issued > BwdSmem::kStages ? issued - BwdSmem::kStages : 0; j < issued; ++j)
           mbar_wait(&b_full[j % BwdSmem::kStages], (j / BwdSmem::kStages) & 1);
       }
@@ -550,6 +728,8 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
     const uint64_t dA1 = desc_sw128(smem_u32(smem + BwdSmem::A));
     const uint64_t dA2 = desc_sw128(smem_u32(smem + BwdSmem::A + 2 * kTileBytes));
     const uint64_t dB = desc_sw128(smem_u32(smem + BwdSmem::B));
+    const uint64_t dAugA = smem_desc(smem_u32(smem + BwdSmem::AugA), kAugLbo, kAugSbo, kSwizzleNone);
+    const uint64_t dAugB = smem_desc(smem_u32(smem + BwdSmem::AugB), kAugLbo, kAugSbo, kSwizzleNone);
     auto tile_b1 = [&](int j) { return dB + static_cast<uint64_t>((j % BwdSmem::kStages) * (2 * kTileBytes >> 4)); };
     auto tile_b2 = [&](int j) { return tile_b1(j) + (kTileBytes >> 4); };
     auto wait_tile = [&](int j) {
@@ -565,179 +745,152 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
       }
       return there;
     };
-    auto scores = [&](uint32_t d, uint64_t da, uint32_t ta, uint64_t db, uint64_t* bar) {
+    // rowsum = 0: S of tile j, 1: dP
+    auto scores = [&](int j, int rowsum) {
       tc_fence_after();
       if (elect_one()) {
+        const uint32_t d = rowsum ? tD : tS;
+        const uint64_t da = rowsum ? dA2 : dA1, db = rowsum ? tile_b2(j) : tile_b1(j);
+        const int st = KEYS ? j % BwdSmem::kStages : 0;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (KEYS)
-            umma_f16(d, da + 2 * kk, db + 2 * kk, idS, kk);
-          else
-            umma_f16_ts(d, ta + 8 * kk, db + 2 * kk, idS, kk);
-        }
-        umma_commit(bar);
+        for (int kk = 0; kk < 4; ++kk) umma_f16(d, da + 2 * kk, db + 2 * kk, idS, kk);
+        umma_f16(d, dAugA + static_cast<uint64_t>(rowsum * (128 * kAugRow >> 4)),
+                 dAugB + static_cast<uint64_t>((2 * st + rowsum) * (BwdSmem::kAugTile >> 4)), idS, 1);
+        umma_commit(rowsum ? dp_full : s_full);
       }
       __syncwarp();
     };
-    // P and dS: columns 32 w .. 32 w + 31 packed at columns 32 w .. 32 w + 15, so
-    // the four 16-row steps start at 0, 8, 32 and 40; each is 16 rows (2048 bytes)
-    // of the streamed tile.
-    auto accumulate = [&](uint32_t d, uint32_t ta, uint64_t db, int j, uint64_t* bar, uint64_t* empty) {
+    // Products over the streamed rows, 16 (2048 bytes of the tile) a step.  Of
+    // columns 32 w .. 32 w + 31 of dP, dS lies packed in the first 16 and P in the
+    // others, so a product's steps start at 0, 8, 32 and 40 from its first.
+    auto accumulate = [&](int j) {
       tc_fence_after();
       if (elect_one()) {
+        const uint64_t db1 = tile_b1(j), db2 = tile_b2(j);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_f16_ts(d, ta + 32 * (kk >> 1) + 8 * (kk & 1), db + static_cast<uint64_t>(128 * kk), idG,
+          umma_f16_ts(tAcc2, tD + 32 * (kk >> 1) + 8 * (kk & 1), db1 + static_cast<uint64_t>(128 * kk), idG,
                       (j > 0 || kk > 0) ? 1u : 0u);
-        if (empty) umma_commit(empty);
-        umma_commit(bar);
+        if (KEYS) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16_ts(tAcc1, tD + 16 + 32 * (kk >> 1) + 8 * (kk & 1), db2 + static_cast<uint64_t>(128 * kk), idG,
+                        (j > 0 || kk > 0) ? 1u : 0u);
+        }
+        umma_commit(acc_done);
+        umma_commit(&b_empty[j % BwdSmem::kStages]);
       }
       __syncwarp();
     };
     auto wait = [&](uint64_t* bar, int j) { return __all_sync(0xffffffffu, mbar_wait(bar, j & 1)); };
-    bool ok = n_sub == 0 || (__all_sync(0xffffffffu, mbar_wait(a_full, 0)) && wait_tile(0));
-    if (ok && n_sub > 0) {
-      scores(tS, dA1, tA1, tile_b1(0), s_full);
-      scores(tD, dA2, tA2, tile_b2(0), dp_full);
+    bool ok = __all_sync(0xffffffffu, mbar_wait(a_full, 0)) && wait_tile(0);
+    if (ok) {
+      scores(0, 0);
+      scores(0, 1);
     }
-    // The next tile's scores run while the warps form this tile's dS, and its dP
-    // while they form the next P, each as soon as its columns are free: those of S
-    // once P's product is done (key CTA) or S has been read (query CTA), those of
-    // dP once dS's product is done.
+    // The next tile's scores run as soon as this tile's have been read, and its dP
+    // once the products of this tile's dS and P, which lie over dP, are done: both
+    // under the elementwise work.
     for (int j = 0; ok && j < n_sub; ++j) {
       const bool more = j + 1 < n_sub;
-      if (!(ok = wait(p_full, j))) break;
-      if (KEYS) accumulate(tAcc1, tS, tile_b2(j), j, v_done, nullptr);
       if (more) {
-        if (!(ok = wait_tile(j + 1) && (!KEYS || wait(v_done, j)))) break;
-        scores(tS, dA1, tA1, tile_b1(j + 1), s_full);
+        if (!(ok = wait(s_read, j) && wait_tile(j + 1))) break;
+        scores(j + 1, 0);
       }
       if (!(ok = wait(ds_full, j))) break;
-      accumulate(tAcc2, tD, tile_b1(j), j, acc_done, &b_empty[j % BwdSmem::kStages]);
+      accumulate(j);
       if (more) {
         if (!(ok = wait(acc_done, j))) break;
-        scores(tD, dA2, tA2, tile_b2(j + 1), dp_full);
+        scores(j + 1, 1);
       }
     }
     if (!ok && lane == 0) atomicOr(a.err, kErrWaitMma);
   } else {
     const int quarter = warp & 3, half = warp >> 2;
-    const int t = tile * 128 + quarter * 32 + lane;
+    const int row = quarter * 32 + lane, t = tile * 128 + row;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const int64_t stat_row = static_cast<int64_t>(bh) * a.tiles * 128;
-    const float scale = BF16 ? 1.0f : ds_scale(a.peak + static_cast<int64_t>(bh) * a.tiles, a.tiles, lane);
-    float row_l = 0.f, row_d = 0.f;
-    if (!KEYS) {
-      // Packed rows of Q (half 0) or dO (half 1) into tensor memory; zeros past the clip.
-      const uint16_t* src = half == 0 ? a.q + b * a.qkv_bs + t * a.qkv_ld : a.dout + b * a.out_bs + t * a.out_ld;
-      uint32_t w[32];
-#pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (t < len) u = *reinterpret_cast<const uint4*>(src + h * kHd + 2 * i);
-        w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
-      }
-      const uint32_t dst = (half == 0 ? tA1 : tA2) + lane_base;
-      tmem_st16_u32(dst, *reinterpret_cast<const uint32_t(*)[16]>(w));
-      tmem_st16_u32(dst + 16, *reinterpret_cast<const uint32_t(*)[16]>(w + 16));
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(a_full);
-      row_l = a.neg_l[stat_row + t];
-      row_d = a.neg_d[stat_row + t];
-    }
+    // fp16: dS is scaled by 2^(up + down).  Up to 2^15 of it goes into P (which is
+    // at most 1, and is as exact scaled as unscaled), and so into dV too; what
+    // shrinks dS is a factor of its own.
+    const int e = BF16 ? 0 : ds_exponent(a.peak + bh * a.tiles, a.tiles, lane);
+    const int up = max(0, min(15, e)), down = min(0, e);
+    const float shift = static_cast<float>(up), shrink = exp2f(static_cast<float>(down));
     bool ok = true;
     for (int j = 0; j < n_sub; ++j) {
-      const float* st_l = reinterpret_cast<const float*>(smem + BwdSmem::STAT + (j % BwdSmem::kStages) * 512) + half * 32;
-      const float* st_d = st_l + 64;
       const int valid = len - j * kSub - half * 32;
       float s[32];
-      uint32_t pk[16];
-      // (KEYS: the statistics came with the streamed tile, whose arrival only the
-      // product warp has seen)
-      if (ok)
-        ok = __all_sync(0xffffffffu, mbar_wait(s_full, j & 1) &&
-                                         (!KEYS || mbar_wait(&b_full[j % BwdSmem::kStages], (j / BwdSmem::kStages) & 1)));
+      uint32_t pk[32];  // dS, then P
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, j & 1));
       if (ok) {
         tc_fence_after();
         tmem_ld32(tS + lane_base + half * 32, s);
       }
-      if (!KEYS) {  // S has been read: its columns are free for the next tile's
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+      tc_fence_before();  // S has been read: its columns are free for the next tile's
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_read);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float2 p = exp2_pair<BWD_POLY>(
+            ffma2(make_float2(s[i], s[i + 1]), make_float2(kC2, kC2), make_float2(shift, shift)), i / 2);
+        s[i] = p.x;
+        s[i + 1] = p.y;
       }
-      if (ok) {
+      // Keys past the clip: their scores are -8 lse, not -infinity, and may overflow.
+      if (!KEYS && valid < 32) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float4 l4 = make_float4(row_l, row_l, row_l, row_l);
-          if (KEYS) l4 = *reinterpret_cast<const float4*>(st_l + i);
-          const float2 x0 = ffma2(make_float2(s[i], s[i + 1]), make_float2(kC2, kC2), make_float2(l4.x, l4.y));
-          const float2 x1 = ffma2(make_float2(s[i + 2], s[i + 3]), make_float2(kC2, kC2), make_float2(l4.z, l4.w));
-          s[i] = ex2_approx(x0.x);
-          s[i + 1] = ex2_approx(x0.y);
-          s[i + 2] = ex2_approx(x1.x);
-          s[i + 3] = ex2_approx(x1.y);
-        }
-        // Keys past the clip: their scores are 0, not -infinity, and 2^neg_l may overflow.
-        if (!KEYS && valid < 32) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i >= valid) s[i] = 0.f;
-        }
-        if (KEYS) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) pk[i / 2] = pack2<BF16>(s[i], s[i + 1]);
-          tmem_st16_u32(tS + lane_base + half * 32, pk);
-        }
+        for (int i = 0; i < 32; ++i)
+          if (i >= valid) s[i] = 0.f;
       }
       if (KEYS) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) pk[16 + i / 2] = pack2<BF16>(s[i], s[i + 1]);
       }
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(dp_full, j & 1));
       if (ok) {
         tc_fence_after();
-        float dp[32];
-        tmem_ld32(tD + lane_base + half * 32, dp);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float4 d4 = make_float4(row_d, row_d, row_d, row_d);
-          if (KEYS) d4 = *reinterpret_cast<const float4*>(st_d + i);
-          float2 g0 = fmul2(fadd2(make_float2(dp[i], dp[i + 1]), make_float2(d4.x, d4.y)), make_float2(s[i], s[i + 1]));
-          float2 g1 =
-              fmul2(fadd2(make_float2(dp[i + 2], dp[i + 3]), make_float2(d4.z, d4.w)), make_float2(s[i + 2], s[i + 3]));
-          if (!BF16) {
-            g0 = fmul2(g0, make_float2(scale, scale));
-            g1 = fmul2(g1, make_float2(scale, scale));
+        for (int c0 = 0; c0 < 32; c0 += 16) {
+          float dp[16];
+          tmem_ld16(tD + lane_base + half * 32 + c0, dp);
+          if (!BF16 && down < 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dp[i] *= shrink;
           }
-          pk[i / 2] = pack2<BF16>(g0.x, g0.y);
-          pk[i / 2 + 1] = pack2<BF16>(g1.x, g1.y);
-        }
-        // A single frame has P = 1 and no gradient through the softmax: dP and
-        // rowsum(dO o O) are the same number there, summed in two orders.
-        if (len == 1) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = 0u;
+          for (int i = 0; i < 16; i += 2) {
+            const float2 g = fmul2(make_float2(dp[i], dp[i + 1]), make_float2(s[c0 + i], s[c0 + i + 1]));
+            pk[(c0 + i) / 2] = pack2<BF16>(g.x, g.y);
+          }
         }
-        tmem_st16_u32(tD + lane_base + half * 32, pk);
+        tmem_st16_u32(tD + lane_base + half * 32, *reinterpret_cast<const uint32_t(*)[16]>(pk));
+        if (KEYS)
+          tmem_st16_u32(tD + lane_base + half * 32 + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);
     }
-    if (n_sub > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_done, (n_sub - 1) & 1));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_done, (n_sub - 1) & 1));
     if (ok) {
       tc_fence_after();
-      const bool write = t < a.T, live = t < len;
-      const int64_t at = b * a.grad_bs + t * a.grad_ld + h * kHd + half * 32;
-      const float back = 0.125f / scale;
-      store_row_part<BF16>(tAcc2 + lane_base + half * 32, (KEYS ? a.dk : a.dq) + at, back, write, live);
-      if (KEYS) store_row_part<BF16>(tAcc1 + lane_base + half * 32, a.dv + at, 1.0f, write, live);
+      const bool live = t < len;
+      // A single frame has P = 1 and no gradient through the softmax: dP and
+      // rowsum(dO o O) are the same number there, summed in two orders.
+      const float unscale = exp2f(static_cast<float>(-up));
+      const float back = len == 1 ? 0.f : 0.125f * unscale * exp2f(static_cast<float>(-down));
+      // over A1 and A2, which no product reads any more
+      stage_row_part<BF16>(tAcc2 + lane_base + half * 32, smem + BwdSmem::A, row, half * 4, back, live);
+      if (KEYS)
+        stage_row_part<BF16>(tAcc1 + lane_base + half * 32, smem + BwdSmem::A + 2 * kTileBytes, row, half * 4, unscale,
+                             live);
     } else if (lane == 0) {
       atomicOr(a.err, kErrWaitSoftmax);
     }
+    named_barrier_sync(1, 256);
+    const int rows = min(128, a.T - tile * 128);
+    const int64_t at = b * a.grad_bs + static_cast<int64_t>(tile) * 128 * a.grad_ld + h * kHd;
+    store_tile(smem + BwdSmem::A, (KEYS ? a.dk : a.dq) + at, a.grad_ld, rows, threadIdx.x, 256);
+    if (KEYS) store_tile(smem + BwdSmem::A + 2 * kTileBytes, a.dv + at, a.grad_ld, rows, threadIdx.x, 256);
   }
 
   tc_fence_before();
@@ -753,12 +906,12 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
 attention_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDo,
                      const __grid_constant__ BwdArgs a) {
-  const int units = a.tiles * a.bh;
-  const int u = blockIdx.x < units ? blockIdx.x : blockIdx.x - units;
-  if (blockIdx.x < units)
-    bwd_body<BF16, true>(tmK, tmV, tmQ, tmDo, a, u % a.tiles, u / a.tiles);
+  // key CTAs, the longer ones, first
+  const int units = a.tiles * a.batch * a.H, u = blockIdx.x;
+  if (u < units)
+    bwd_body<BF16, true>(tmK, tmV, tmQ, tmDo, a, u);
   else
-    bwd_body<BF16, false>(tmQ, tmDo, tmK, tmV, a, u % a.tiles, u / a.tiles);
+    bwd_body<BF16, false>(tmQ, tmDo, tmK, tmV, a, u - units);
 }
 
 // [batch][T][H][64] operand as {H * 64, T, batch}, 64-row boxes of one head.
@@ -784,12 +937,12 @@ cudaError_t launch_attention_fwd(const AttnTrain& s, const void* q, const void* 
     return r;
   const int tiles = (s.T + 127) / 128;
   return launch_pdl(kernel, dim3(tiles * s.batch * s.H), dim3(kFwdThreads), FwdSmem::TOTAL, st, tq, tk, tv, s.frames,
-                    s.T, s.H, tiles, static_cast<uint16_t*>(out), s.out_ld, s.out_bs, lse, err);
+                    s.T, s.H, s.batch, tiles, static_cast<uint16_t*>(out), s.out_ld, s.out_bs, lse, err);
 }
 
 size_t attention_bwd_ws_bytes(int batch, int T, int H) {
   const size_t tiles = (static_cast<size_t>(T) + 127) / 128, bh = static_cast<size_t>(batch) * H;
-  return bh * tiles * (128 * 2 * sizeof(float) + sizeof(float2));
+  return bh * tiles * (128 * 2 * kAugRow + sizeof(float2));
 }
 
 cudaError_t launch_attention_bwd(const AttnTrain& s, const void* dout, const void* q, const void* k, const void* v,
@@ -803,28 +956,24 @@ cudaError_t launch_attention_bwd(const AttnTrain& s, const void* dout, const voi
   if ((r = map_rows(&td, dout, s.out_ld, s.out_bs, s)) != cudaSuccess) return r;
   const int tiles = (s.T + 127) / 128, bh = s.batch * s.H;
   const int64_t rows = static_cast<int64_t>(bh) * tiles * 128;
-  float* neg_l = static_cast<float*>(ws);
-  float* neg_d = neg_l + rows;
-  float2* peak = reinterpret_cast<float2*>(neg_d + rows);
+  uint8_t* aug_l = static_cast<uint8_t*>(ws);
+  uint8_t* aug_d = aug_l + rows * kAugRow;
+  float2* peak = reinterpret_cast<float2*>(aug_d + rows * kAugRow);
   auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
   r = launch_pdl(s.bf16 ? attention_bwd_rows_kernel<true> : attention_bwd_rows_kernel<false>, dim3(tiles * bh),
                  dim3(256), 0, st, u16(dout), u16(out), s.out_ld, s.out_bs, u16(v), s.qkv_ld, s.qkv_bs, lse, s.frames,
-                 s.T, s.H, tiles, neg_l, neg_d, peak);
+                 s.T, s.H, tiles, aug_l, aug_d, peak);
   if (r != cudaSuccess) return r;
   BwdArgs a;
-  a.q = u16(q);
-  a.dout = u16(dout);
   a.dq = static_cast<uint16_t*>(dq);
   a.dk = static_cast<uint16_t*>(dk);
   a.dv = static_cast<uint16_t*>(dv);
-  a.qkv_ld = s.qkv_ld; a.qkv_bs = s.qkv_bs;
-  a.out_ld = s.out_ld; a.out_bs = s.out_bs;
   a.grad_ld = s.grad_ld; a.grad_bs = s.grad_bs;
   a.frames = s.frames;
-  a.neg_l = neg_l;
-  a.neg_d = neg_d;
+  a.aug_l = aug_l;
+  a.aug_d = aug_d;
   a.peak = peak;
-  a.T = s.T; a.H = s.H; a.tiles = tiles; a.bh = bh;
+  a.T = s.T; a.H = s.H; a.batch = s.batch; a.tiles = tiles;
   a.err = err;
   auto kernel = s.bf16 ? attention_bwd_kernel<true> : attention_bwd_kernel<false>;
   if ((r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem::TOTAL)) != cudaSuccess)
