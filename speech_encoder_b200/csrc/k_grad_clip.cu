@@ -15,7 +15,7 @@ namespace {
 constexpr int kClipThreads = 256;
 constexpr int kChunk = 8192;        // elements of one tensor that a block takes at a time
 constexpr int kTable = 512;         // tensors per launch
-constexpr int kNormBlocks = 2 * kNumSMs;
+constexpr int kBlocks = 4 * kNumSMs;  // of 256 threads, resident at once
 
 struct ClipTable {
   const void* src[kTable];
@@ -74,6 +74,20 @@ __device__ __forceinline__ void chunk_range(const T* src, int64_t n, int c, int6
   *to = end < n ? end : n;
 }
 
+// A whole chunk's 16-byte vectors per thread: all loaded before any is used.
+template <typename T>
+constexpr int kVecs = kChunk * static_cast<int>(sizeof(T)) / 16 / kClipThreads;
+
+template <typename T>
+__device__ __forceinline__ double square(T v) {
+  const double x = Elem<T>::get(v);
+  return x * x;
+}
+
+// Squares of one thread's part of a chunk.  32 of them are added in fp32 where that
+// is safe: a sum between 1e-20 and 1e37 has no overflowed square, and squares lost
+// below fp32's range (each below 1e-38) do not show in it.  Otherwise, and across
+// parts, in fp64 (all in fp64 took 257 us for 1.2 GB, bound by its conversions).
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const void* srcv, int64_t n, int c) {
   constexpr int V = 16 / sizeof(T);
@@ -81,25 +95,46 @@ __device__ __forceinline__ double chunk_squares(const void* srcv, int64_t n, int
   int64_t head, from, to;
   chunk_range<T>(src, n, c, &head, &from, &to);
   double s = 0.0;
-  if (c == 0 && threadIdx.x < head) {
-    const double x = Elem<T>::get(src[threadIdx.x]);
-    s = x * x;
-  }
-  const int64_t vecs = (to - from) / V;
-#pragma unroll 4
-  for (int64_t i = threadIdx.x; i < vecs; i += kClipThreads) {
-    const Vec16<T> u = *reinterpret_cast<const Vec16<T>*>(src + from + i * V);
+  if (c == 0 && threadIdx.x < head) s = square<T>(src[threadIdx.x]);
+  if (to <= from) return s;
+  const int vecs = static_cast<int>(to - from) / V;
+  const Vec16<T>* p = reinterpret_cast<const Vec16<T>*>(src + from);
+  Vec16<T> u[kVecs<T>];
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const double x = Elem<T>::get(u.v[k]);
-      s = fma(x, x, s);
+  for (int i = 0; i < kVecs<T>; ++i) {
+    const int at = threadIdx.x + i * kClipThreads;
+    if (at < vecs) {
+      u[i] = p[at];
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) u[i].v[k] = Elem<T>::put(0.f);
     }
   }
-  const int64_t at = from + vecs * V + threadIdx.x;
-  if (at < to) {
-    const double x = Elem<T>::get(src[at]);
-    s = fma(x, x, s);
+  float q[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) q[k] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kVecs<T>; ++i) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const float x = Elem<T>::get(u[i].v[k]);
+      q[k] = fmaf(x, x, q[k]);
+    }
   }
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < V; ++k) sum += q[k];
+  if (sum > 1e-20f && sum < 1e37f) {
+    s += sum;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVecs<T>; ++i) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) s += square<T>(u[i].v[k]);
+    }
+  }
+  const int64_t at = from + static_cast<int64_t>(vecs) * V + threadIdx.x;
+  if (at < to) s += square<T>(src[at]);
   return s;
 }
 
@@ -111,21 +146,30 @@ __device__ __forceinline__ void chunk_scale(const void* srcv, void* dstv, int64_
   int64_t head, from, to;
   chunk_range<T>(src, n, c, &head, &from, &to);
   if (c == 0 && threadIdx.x < head) dst[threadIdx.x] = Elem<T>::put(Elem<T>::get(src[threadIdx.x]) * f);
-  const int64_t vecs = (to - from) / V;
+  if (to <= from) return;
+  const int vecs = static_cast<int>(to - from) / V;
   const bool same = ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) == 0;
-#pragma unroll 4
-  for (int64_t i = threadIdx.x; i < vecs; i += kClipThreads) {
-    Vec16<T> u = *reinterpret_cast<const Vec16<T>*>(src + from + i * V);
+  const Vec16<T>* p = reinterpret_cast<const Vec16<T>*>(src + from);
+  Vec16<T> u[kVecs<T>];
 #pragma unroll
-    for (int k = 0; k < V; ++k) u.v[k] = Elem<T>::put(Elem<T>::get(u.v[k]) * f);
+  for (int i = 0; i < kVecs<T>; ++i) {
+    const int at = threadIdx.x + i * kClipThreads;
+    if (at < vecs) u[i] = p[at];
+  }
+#pragma unroll
+  for (int i = 0; i < kVecs<T>; ++i) {
+    const int at = threadIdx.x + i * kClipThreads;
+    if (at >= vecs) break;
+#pragma unroll
+    for (int k = 0; k < V; ++k) u[i].v[k] = Elem<T>::put(Elem<T>::get(u[i].v[k]) * f);
     if (same) {
-      *reinterpret_cast<Vec16<T>*>(dst + from + i * V) = u;
+      reinterpret_cast<Vec16<T>*>(dst + from)[at] = u[i];
     } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k) dst[from + i * V + k] = u.v[k];
+      for (int k = 0; k < V; ++k) dst[from + static_cast<int64_t>(at) * V + k] = u[i].v[k];
     }
   }
-  const int64_t at = from + vecs * V + threadIdx.x;
+  const int64_t at = from + static_cast<int64_t>(vecs) * V + threadIdx.x;
   if (at < to) dst[at] = Elem<T>::put(Elem<T>::get(src[at]) * f);
 }
 
@@ -142,8 +186,8 @@ __device__ __forceinline__ double block_sum(double s) {
   return s;
 }
 
-// Sums in fp64: squares of fp32 and bf16 values leave fp32's range from 1.8e19
-// and below 1e-23, and the sum may have 10^9 terms.
+// The sum is fp64: squares of fp32 and bf16 values leave fp32's range from 1.8e19
+// and below 1e-23, and there may be 10^9 of them.
 __global__ void __launch_bounds__(kClipThreads)
 grad_squares_kernel(const __grid_constant__ ClipTable t, double* __restrict__ partial) {
   if (threadIdx.x == 0) pdl_launch_dependents();
@@ -175,7 +219,9 @@ grad_scale_kernel(const __grid_constant__ ClipTable t, const double* __restrict_
   double by = static_cast<double>(max_norm) / (norm + 1e-6);
   if (!(by < 1.0) || !(norm < INFINITY)) by = 1.0;  // not clipped, or not a finite norm
   const float f = static_cast<float>(by * static_cast<double>(scale));
-  for (int c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
+  // from the end, where the first pass has just been: what it left in L2 is not
+  // read from memory again
+  for (int c = t.first[t.count] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= static_cast<int>(gridDim.x)) {
     const int i = find_tensor(t, c);
     const int k = c - t.first[i];
     if (f == 1.0f && t.src[i] == t.dst[i]) continue;  // in place and unchanged
@@ -192,7 +238,7 @@ grad_scale_kernel(const __grid_constant__ ClipTable t, const double* __restrict_
 
 size_t grad_clip_ws_bytes(int n) {
   const size_t tables = n <= kTable ? 1 : (static_cast<size_t>(n) + kTable - 1) / kTable;
-  return tables * kNormBlocks * sizeof(double);
+  return tables * kBlocks * sizeof(double);
 }
 
 cudaError_t launch_grad_clip(int n, const void* const* grads, void* const* outs, const int64_t* counts,
@@ -223,14 +269,14 @@ cudaError_t launch_grad_clip(int n, const void* const* grads, void* const* outs,
   };
   for (int k = 0; k < tables; ++k) {
     fill(k);
-    const cudaError_t r = launch_pdl(grad_squares_kernel, dim3(kNormBlocks), dim3(kClipThreads), 0, st, t,
-                                     partial + static_cast<int64_t>(k) * kNormBlocks);
+    const cudaError_t r = launch_pdl(grad_squares_kernel, dim3(kBlocks), dim3(kClipThreads), 0, st, t,
+                                     partial + static_cast<int64_t>(k) * kBlocks);
     if (r != cudaSuccess) return r;
   }
   for (int k = tables - 1; k >= 0; --k) {
     if (tables > 1) fill(k);
-    const cudaError_t r = launch_pdl(grad_scale_kernel, dim3(kNormBlocks), dim3(kClipThreads), 0, st, t,
-                                     static_cast<const double*>(partial), tables * kNormBlocks, scale, max_norm, norm);
+    const cudaError_t r = launch_pdl(grad_scale_kernel, dim3(kBlocks), dim3(kClipThreads), 0, st, t,
+                                     static_cast<const double*>(partial), tables * kBlocks, scale, max_norm, norm);
     if (r != cudaSuccess) return r;
   }
   return cudaSuccess;

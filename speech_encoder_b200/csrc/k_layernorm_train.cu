@@ -39,36 +39,129 @@ struct alignas(sizeof(T) * V) Vec {
   T v[V];
 };
 
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float* out) {
-  const Vec<T, V> u = *reinterpret_cast<const Vec<T, V>*>(p);
+// A thread's elements of a row: NCH chunks of V, chunk i at column (lane + G i) V;
+// columns past the end read as zero and are not written.
+template <typename T, int V, int NCH, int G>
+__device__ __forceinline__ void load_row(const T* p, int lane, int cols, Vec<T, V> (&u)[NCH]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) out[i] = to_f32<T>(u.v[i]);
+  for (int i = 0; i < NCH; ++i) {
+    const int c = (lane + G * i) * V;
+    if (c < cols) {
+      u[i] = *reinterpret_cast<const Vec<T, V>*>(p + c);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) u[i].v[k] = from_f32<T>(0.f);
+    }
+  }
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float* in) {
-  Vec<T, V> u;
+template <typename T, int V, int NCH>
+__device__ __forceinline__ void widen(const Vec<T, V> (&u)[NCH], float2 (&out)[NCH * V / 2]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) u.v[i] = from_f32<T>(in[i]);
-  *reinterpret_cast<Vec<T, V>*>(p) = u;
+  for (int e = 0; e < NCH * V; e += 2)
+    out[e / 2] = make_float2(to_f32<T>(u[e / V].v[e % V]), to_f32<T>(u[(e + 1) / V].v[(e + 1) % V]));
 }
 
-// GELU with the accuracy of fp32: the tanh form as z sigmoid(2u),
-// u = sqrt(2/pi) (z + 0.044715 z^3).
-__device__ __forceinline__ float gelu_value(float z, int act) {
-  if (act == 1) return gelu_erf(z);
-  const float k = 0.7978845608028654f;
-  return z * rcp_approx(1.0f + __expf(-2.0f * z * fmaf(0.044715f * k, z * z, k)));
+template <typename T, int V, int NCH, int G>
+__device__ __forceinline__ void store_row(T* p, int lane, int cols, const float2 (&in)[NCH * V / 2]) {
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = (lane + G * i) * V;
+    if (c < cols) {
+      Vec<T, V> u;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int e = i * V + k;
+        u.v[k] = from_f32<T>(e & 1 ? in[e / 2].y : in[e / 2].x);
+      }
+      *reinterpret_cast<Vec<T, V>*>(p + c) = u;
+    }
+  }
+}
+
+// Elements e .. e + 3 of a thread's part of a vector over the columns.
+template <int V, int G>
+__device__ __forceinline__ float4 load4(const float* p, int lane, int cols, int e) {
+  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (V >= 4) {
+    const int c = (lane + G * (e / V)) * V;
+    if (c < cols) r = *reinterpret_cast<const float4*>(p + c + e % V);
+  } else {
+    if (lane + G * e < cols) r.x = p[lane + G * e];
+    if (lane + G * (e + 1) < cols) r.y = p[lane + G * (e + 1)];
+    if (lane + G * (e + 2) < cols) r.z = p[lane + G * (e + 2)];
+    if (lane + G * (e + 3) < cols) r.w = p[lane + G * (e + 3)];
+  }
+  return r;
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Pairs of elements in packed fp32 instructions: with scalar ones both GELU passes
+// over 51199 x 512 were bound by instruction issue.
+//
+// h = Phi(-|z|) and e = exp(-z^2 / 2) for the exact GELU and its slope, which share
+// one exponential: erfc by formula 7.1.26 of Abramowitz and Stegun's Handbook
+// (Hastings), a polynomial in 1 / (1 + p x) times e, absolute error below 0.75e-7
+// in Phi.
+__device__ __forceinline__ float2 normal_tail(float2 z, float2 x, float2* e) {
+  const float2 d = ffma2(x, both(0.3275911f * 0.70710678118654752f), both(1.0f));
+  const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  const float2 a = fmul2(fmul2(z, both(-0.5f * 1.4426950408889634f)), z);
+  *e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+  float2 p = ffma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+  p = ffma2(p, t, both(0.5f * 1.421413741f));
+  p = ffma2(p, t, both(0.5f * -0.284496736f));
+  p = ffma2(p, t, both(0.5f * 0.254829592f));
+  return fmul2(fmul2(p, t), *e);
+}
+
+// The tanh form is z sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3): the sigmoid.
+__device__ __forceinline__ float2 tanh_gate(float2 z, float2 z2) {
+  constexpr float k = -2.0f * 0.7978845608028654f * 1.4426950408889634f;
+  const float2 a = fmul2(z, ffma2(z2, both(0.044715f * k), both(k)));
+  const float2 d = fadd2(make_float2(ex2_approx(a.x), ex2_approx(a.y)), both(1.0f));
+  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
+
+// GELU: z Phi(z) = max(z, 0) - |z| Phi(-|z|).
+template <int ACT>
+__device__ __forceinline__ float2 gelu_value(float2 z) {
+  if (ACT == 1) {
+    const float2 x = make_float2(fabsf(z.x), fabsf(z.y));
+    float2 e;
+    const float2 h = normal_tail(z, x, &e);
+    return ffma2(make_float2(-x.x, -x.y), h, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+  }
+  if (ACT == 2) return fmul2(z, tanh_gate(z, fmul2(z, z)));
+  return z;
 }
 
 // f'(z): Phi(z) + z phi(z), or s + z s (1 - s) 2 u'(z) with s = sigmoid(2u).
-__device__ __forceinline__ float gelu_slope(float z, int act) {
-  if (act == 1)
-    return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * 0.70710678118654752f)));
-  const float k = 0.7978845608028654f, z2 = z * z;
-  const float s = rcp_approx(1.0f + __expf(-2.0f * z * fmaf(0.044715f * k, z2, k)));
-  return fmaf(z * s * (1.0f - s), 2.0f * fmaf(3.0f * 0.044715f * k, z2, k), s);
+template <int ACT>
+__device__ __forceinline__ float2 gelu_slope(float2 z) {
+  if (ACT == 1) {
+    float2 e;
+    const float2 h = normal_tail(z, make_float2(fabsf(z.x), fabsf(z.y)), &e);
+    const float2 q = ffma2(h, both(-1.0f), both(0.5f));
+    const float2 phi = fadd2(make_float2(copysignf(q.x, z.x), copysignf(q.y, z.y)), both(0.5f));
+    return ffma2(fmul2(z, both(0.3989422804014327f)), e, phi);
+  }
+  constexpr float k = 0.7978845608028654f;
+  const float2 z2 = fmul2(z, z), s = tanh_gate(z, z2);
+  const float2 r = fmul2(fmul2(z, s), ffma2(s, both(-1.0f), both(1.0f)));
+  return ffma2(r, ffma2(z2, both(6.0f * 0.044715f * k), both(2.0f * k)), s);
+}
+
+// fn(std::integral_constant<int, act>()), so that the choice is made once a row.
+template <typename F>
+__device__ __forceinline__ void by_act(int act, F&& fn) {
+  if (act == 0)
+    fn(std::integral_constant<int, 0>());
+  else if (act == 1)
+    fn(std::integral_constant<int, 1>());
+  else
+    fn(std::integral_constant<int, 2>());
 }
 
 // Sum over the G threads of a row (a warp, or the whole block).
@@ -88,8 +181,14 @@ __device__ __forceinline__ float group_sum(float v, float* red) {
 
 constexpr int kLnThreads = 256;
 
-// G threads a row, each with NCH chunks of V elements (chunk i at column
-// (thread + G i) V).
+// Chunks a thread is given at a time: its 1 to 4 steps cover a row with at most the
+// last step's chunks past the end.
+template <typename X>
+__host__ __device__ constexpr int chunk_step() {
+  return sizeof(X) == 4 ? 2 : 1;
+}
+
+// G threads a row, each with NCH chunks of V elements.
 template <typename X, typename Y, int V, int NCH, int G>
 __global__ void __launch_bounds__(kLnThreads)
 layernorm_fwd_kernel(const X* __restrict__ x, int64_t x_ld, Y* __restrict__ y, int64_t y_ld, int64_t rows, int cols,
@@ -101,166 +200,172 @@ layernorm_fwd_kernel(const X* __restrict__ x, int64_t x_ld, Y* __restrict__ y, i
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kLnThreads / G) + threadIdx.x / G;
   pdl_wait();
   if (row >= rows) return;  // whole groups
-  const X* xr = x + row * x_ld;
-  float v[NCH * V];
-  float s = 0.f;
+  constexpr int NP = NCH * V / 2;
+  Vec<X, V> raw[NCH];
+  load_row<X, V, NCH, G>(x + row * x_ld, lane, cols, raw);
+  float2 v[NP];
+  widen<X, V, NCH>(raw, v);
+  float2 s = v[0];
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = (lane + G * i) * V;
-    if (c < cols) {
-      load_vec<X, V>(xr + c, v + i * V);
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[i * V + k] = 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < V; ++k) s += v[i * V + k];
-  }
+  for (int i = 1; i < NP; ++i) s = fadd2(s, v[i]);
   const float inv = 1.0f / cols;
-  const float mean = group_sum<G>(s, red) * inv;
-  float q = 0.f;
+  const float mean = group_sum<G>(s.x + s.y, red) * inv;
+  float2 q = both(0.f);
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    if ((lane + G * i) * V < cols) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) q += (v[i * V + k] - mean) * (v[i * V + k] - mean);
+  for (int i = 0; i < NP; ++i) {
+    v[i] = fadd2(v[i], both(-mean));
+    // columns past the end, which can only be in the last chunks (see by_chunks)
+    const int e = 2 * i;
+    if (V == 1 || e / V >= NCH - chunk_step<X>()) {
+      if ((lane + G * (e / V)) * V >= cols) v[i].x = 0.f;
+      if ((lane + G * ((e + 1) / V)) * V >= cols) v[i].y = 0.f;
     }
+    q = ffma2(v[i], v[i], q);
   }
-  const float rstd = 1.0f / sqrtf(group_sum<G>(q, red) * inv + eps);
+  const float var = group_sum<G>(q.x + q.y, red) * inv;
+  const float rstd = 1.0f / sqrtf(var + eps);
   if (lane == 0) {
     mean_out[row] = mean;
     rstd_out[row] = rstd;
   }
-  Y* yr = y + row * y_ld;
+  Vec<float, V> gv[NCH], bv[NCH];
+  load_row<float, V, NCH, G>(gamma, lane, cols, gv);
+  load_row<float, V, NCH, G>(beta, lane, cols, bv);
+  float2 g[NP], b[NP];
+  widen<float, V, NCH>(gv, g);
+  widen<float, V, NCH>(bv, b);
+  by_act(act, [&](auto a) {
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = (lane + G * i) * V;
-    if (c < cols) {
-      float g[V], b[V];
-      load_vec<float, V>(gamma + c, g);
-      load_vec<float, V>(beta + c, b);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float z = fmaf((v[i * V + k] - mean) * rstd, g[k], b[k]);
-        g[k] = act ? gelu_value(z, act) : z;
-      }
-      store_vec<Y, V>(yr + c, g);
-    }
-  }
+    for (int i = 0; i < NP; ++i) v[i] = gelu_value<decltype(a)::value>(ffma2(fmul2(v[i], both(rstd)), g[i], b[i]));
+  });
+  store_row<Y, V, NCH, G>(y + row * y_ld, lane, cols, v);
 }
 
 // Persistent blocks: each thread keeps its columns' dgamma and dbeta over all
-// the rows it sees; the block adds its groups' sums in order and leaves one
-// partial per block, which layernorm_affine_kernel adds up in block order.
+// the rows it sees, with the next row's elements on their way while one is worked
+// on; the block adds its groups' sums in order and leaves one partial per block,
+// which layernorm_affine_kernel adds up in block order.
 template <typename X, typename Y, int V, int NCH, int G>
-__global__ void __launch_bounds__(kLnThreads)
+__global__ void __launch_bounds__(kLnThreads, NCH * V <= 16 ? 2 : 1)
 layernorm_bwd_kernel(const Y* __restrict__ dy, int64_t dy_ld, const X* __restrict__ x, int64_t x_ld, int64_t rows,
                      int cols, const float* __restrict__ gamma, const float* __restrict__ beta,
-                     const float* __restrict__ mean, const float* __restrict__ rstd, int act,
-                     const X* dres, int64_t dres_ld, X* dx, int64_t dx_ld,
-                     float* __restrict__ partial) {
-  extern __shared__ float acc[];  // [2][cols] when several groups share the block
+                     const float* __restrict__ mean, const float* __restrict__ rstd, int act, const X* dres,
+                     int64_t dres_ld, X* dx, int64_t dx_ld, float* __restrict__ partial) {
+  extern __shared__ float acc[];  // [groups][2][cols] when several groups share the block
   __shared__ float red[kLnThreads / 32];
   if (threadIdx.x == 0) pdl_launch_dependents();
   constexpr int kGroups = kLnThreads / G;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
-  float dg[NCH * V], db[NCH * V];
+  constexpr int NP = NCH * V / 2;
+  float2 dg[NP], db[NP];
 #pragma unroll
-  for (int i = 0; i < NCH * V; ++i) dg[i] = db[i] = 0.f;
+  for (int i = 0; i < NP; ++i) dg[i] = db[i] = both(0.f);
   const float inv = 1.0f / cols;
+  Vec<X, V> xn[NCH];
+  Vec<Y, V> yn[NCH];
+  float mn = 0.f, rn = 0.f;
+  auto fetch = [&](int64_t row) {
+    mn = mean[row];
+    rn = rstd[row];
+    load_row<X, V, NCH, G>(x + row * x_ld, lane, cols, xn);
+    load_row<Y, V, NCH, G>(dy + row * dy_ld, lane, cols, yn);
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + group;
   pdl_wait();
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + group; row < rows;
-       row += static_cast<int64_t>(gridDim.x) * kGroups) {
-    const float m = mean[row], r = rstd[row];
-    float xh[NCH * V], w[NCH * V];
-    float s1 = 0.f, s2 = 0.f;
+  if (row < rows) fetch(row);
+  for (; row < rows; row += step) {
+    const float r = rn, m = mn;
+    float2 xh[NP], w[NP];
+    widen<X, V, NCH>(xn, xh);
+    widen<Y, V, NCH>(yn, w);
+    if (row + step < rows) fetch(row + step);
+    float2 s1 = both(0.f), s2 = both(0.f);
+    // (columns past the end: dy is 0, so they add nothing)
+    by_act(act, [&](auto a) {
+      constexpr int ACT = decltype(a)::value;
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = (lane + G * i) * V;
-      if (c < cols) {
-        load_vec<X, V>(x + row * x_ld + c, xh + i * V);
-        load_vec<Y, V>(dy + row * dy_ld + c, w + i * V);
-      }
-    }
+      for (int e = 0; e < 2 * NP; e += 4) {
+        const float4 g4 = load4<V, G>(gamma, lane, cols, e);
+        float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ACT != 0) b4 = load4<V, G>(beta, lane, cols, e);
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = (lane + G * i) * V;
-      if (c < cols) {
-        float g[V], b[V];
-        load_vec<float, V>(gamma + c, g);
-        if (act) load_vec<float, V>(beta + c, b);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const int e = i * V + k;
-          xh[e] = (xh[e] - m) * r;
-          if (act) w[e] *= gelu_slope(fmaf(xh[e], g[k], b[k]), act);
-          dg[e] = fmaf(w[e], xh[e], dg[e]);
-          db[e] += w[e];
-          w[e] *= g[k];
-          s1 += w[e];
-          s2 = fmaf(w[e], xh[e], s2);
+        for (int i = e / 2; i < e / 2 + 2; ++i) {
+          const float2 g = i & 1 ? make_float2(g4.z, g4.w) : make_float2(g4.x, g4.y);
+          const float2 b = i & 1 ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y);
+          xh[i] = fmul2(fadd2(xh[i], both(-m)), both(r));
+          if (ACT != 0) w[i] = fmul2(w[i], gelu_slope<ACT>(ffma2(xh[i], g, b)));
+          dg[i] = ffma2(w[i], xh[i], dg[i]);
+          db[i] = fadd2(db[i], w[i]);
+          w[i] = fmul2(w[i], g);
+          s1 = fadd2(s1, w[i]);
+          s2 = ffma2(w[i], xh[i], s2);
         }
       }
+    });
+    const float c1 = group_sum<G>(s1.x + s1.y, red) * inv;
+    const float c2 = group_sum<G>(s2.x + s2.y, red) * inv;
+    if (dres) {
+      Vec<X, V> rv[NCH];
+      load_row<X, V, NCH, G>(dres + row * dres_ld, lane, cols, rv);
+      float2 res[NP];
+      widen<X, V, NCH>(rv, res);
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        w[i] = ffma2(both(r), ffma2(xh[i], both(-c2), fadd2(w[i], both(-c1))), res[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) w[i] = fmul2(both(r), ffma2(xh[i], both(-c2), fadd2(w[i], both(-c1))));
     }
-    s1 = group_sum<G>(s1, red) * inv;
-    s2 = group_sum<G>(s2, red) * inv;
+    store_row<X, V, NCH, G>(dx + row * dx_ld, lane, cols, w);
+  }
+  float* mine = partial + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+  float* sums = kGroups > 1 ? acc + group * 2 * cols : mine;
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = (lane + G * i) * V;
-      if (c < cols) {
-        float o[V];
-        if (dres) {
-          load_vec<X, V>(dres + row * dres_ld + c, o);
-        } else {
+  for (int i = 0; i < NCH; ++i) {
+    const int c = (lane + G * i) * V;
+    if (c < cols) {
 #pragma unroll
-          for (int k = 0; k < V; ++k) o[k] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = fmaf(r, w[i * V + k] - s1 - xh[i * V + k] * s2, o[k]);
-        store_vec<X, V>(dx + row * dx_ld + c, o);
+      for (int k = 0; k < V; ++k) {
+        const int e = i * V + k;
+        sums[c + k] = e & 1 ? dg[e / 2].y : dg[e / 2].x;
+        sums[cols + c + k] = e & 1 ? db[e / 2].y : db[e / 2].x;
       }
     }
   }
-  float* mine = partial + static_cast<int64_t>(blockIdx.x) * 2 * cols;
-  for (int turn = 0; turn < kGroups; ++turn) {
-    if (group == turn) {
-      const bool first = turn == 0, last = turn == kGroups - 1;
+  if (kGroups > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * cols; c += kLnThreads) {
+      float v = acc[c];
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const int c = (lane + G * i) * V + k;
-          if (c < cols) {
-            const float a = dg[i * V + k] + (first ? 0.f : acc[c]), d = db[i * V + k] + (first ? 0.f : acc[cols + c]);
-            (last ? mine : acc)[c] = a;
-            (last ? mine : acc)[cols + c] = d;
-          }
-        }
-      }
+      for (int i = 1; i < kGroups; ++i) v += acc[i * 2 * cols + c];
+      mine[c] = v;
     }
-    if (kGroups > 1) __syncthreads();
   }
 }
 
-// dgamma and dbeta: the blocks' partials added in a fixed order.  A block takes
-// 32 columns of the 2 cols; 8 warps add every eighth partial, then warp 0 the 8.
-__global__ void __launch_bounds__(256)
+// dgamma and dbeta: the blocks' partials added in a fixed order.  A block takes 32
+// columns of the 2 cols; 16 warps add every 16th partial, then warp 0 the 16.
+constexpr int kAffineWarps = 16;
+__global__ void __launch_bounds__(32 * kAffineWarps)
 layernorm_affine_kernel(const float* __restrict__ partial, int blocks, int cols, float* __restrict__ dgamma,
                         float* __restrict__ dbeta) {
-  __shared__ float red[8][32];
+  __shared__ float red[kAffineWarps][32];
   if (threadIdx.x == 0) pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
   pdl_wait();
   float s = 0.f;
-  if (c < 2 * cols)
-    for (int i = warp; i < blocks; i += 8) s += partial[static_cast<int64_t>(i) * 2 * cols + c];
+  if (c < 2 * cols) {
+#pragma unroll 8
+    for (int i = warp; i < blocks; i += kAffineWarps) s += partial[static_cast<int64_t>(i) * 2 * cols + c];
+  }
   red[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < 2 * cols) {
     s = red[0][lane];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][lane];
+    for (int i = 1; i < kAffineWarps; ++i) s += red[i][lane];
     (c < cols ? dgamma + c : dbeta + (c - cols))[0] = s;
   }
 }
@@ -271,7 +376,7 @@ layernorm_affine_kernel(const float* __restrict__ partial, int blocks, int cols,
 template <typename X, int G, typename F>
 cudaError_t by_chunks(bool vec, int cols, F&& fn) {
   constexpr int V = 16 / sizeof(X);
-  constexpr int kStep = sizeof(X) == 4 ? 2 : 1;  // chunks per thread: 1..4 (16-bit), 2, 4, 6, 8 (fp32)
+  constexpr int kStep = chunk_step<X>();
   if (!vec) return fn(std::integral_constant<int, 1>(), std::integral_constant<int, 32>());
   const int n = (cols + G * V * kStep - 1) / (G * V * kStep);
   std::integral_constant<int, V> v;
@@ -287,10 +392,12 @@ constexpr int kWarpCols = 1024;
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// Blocks of the backward pass: what is resident at once (see its launch bounds).
 int bwd_blocks(int64_t rows, int cols) {
   const int per = cols <= kWarpCols ? kLnThreads / 32 : 1;
+  const int64_t most = cols <= kWarpCols / 2 ? 2 * kNumSMs : kNumSMs;
   const int64_t want = (rows + per - 1) / per;
-  return static_cast<int>(want < 2 * kNumSMs ? (want < 1 ? 1 : want) : 2 * kNumSMs);
+  return static_cast<int>(want < most ? (want < 1 ? 1 : want) : most);
 }
 
 template <typename X, typename Y, int G>
@@ -325,10 +432,15 @@ cudaError_t bwd(const LnTrain& s, const BwdPtrs& p, cudaStream_t st) {
   const bool vec = s.cols % V == 0 && s.x_ld % V == 0 && s.y_ld % V == 0 && p.dx_ld % V == 0 &&
                    (!p.dres || (p.dres_ld % V == 0 && aligned(p.dres, 16))) && aligned(p.x, 16) && aligned(p.dx, 16) &&
                    aligned(p.dy, V * sizeof(Y)) && aligned(s.gamma, 4 * V) && aligned(s.beta, 4 * V);
-  const size_t smem = G == 32 ? 2 * static_cast<size_t>(s.cols) * sizeof(float) : 0;
+  const size_t smem = G == 32 ? kLnThreads / 32 * 2 * static_cast<size_t>(s.cols) * sizeof(float) : 0;
   return by_chunks<X, G>(vec, s.cols, [&](auto v, auto nch) {
-    return launch_pdl(layernorm_bwd_kernel<X, Y, decltype(v)::value, decltype(nch)::value, G>,
-                      dim3(bwd_blocks(s.rows, s.cols)), dim3(kLnThreads), smem, st, static_cast<const Y*>(p.dy), s.y_ld,
+    auto kernel = layernorm_bwd_kernel<X, Y, decltype(v)::value, decltype(nch)::value, G>;
+    if (smem > 48 * 1024) {
+      const cudaError_t r =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (r != cudaSuccess) return r;
+    }
+    return launch_pdl(kernel, dim3(bwd_blocks(s.rows, s.cols)), dim3(kLnThreads), smem, st, static_cast<const Y*>(p.dy), s.y_ld,
                       static_cast<const X*>(p.x), s.x_ld, s.rows, s.cols, s.gamma, s.beta, p.mean, p.rstd, s.act,
                       static_cast<const X*>(p.dres), p.dres_ld, static_cast<X*>(p.dx), p.dx_ld, p.partial);
   });
@@ -371,7 +483,7 @@ cudaError_t launch_layernorm_bwd(const LnTrain& s, const void* dy, const void* x
     return s.cols <= kWarpCols ? bwd<X, Y, 32>(s, p, st) : bwd<X, Y, kLnThreads>(s, p, st);
   });
   if (r != cudaSuccess) return r;
-  return launch_pdl(layernorm_affine_kernel, dim3((2 * s.cols + 31) / 32), dim3(256), 0, st, p.partial,
+  return launch_pdl(layernorm_affine_kernel, dim3((2 * s.cols + 31) / 32), dim3(32 * kAffineWarps), 0, st, p.partial,
                     bwd_blocks(s.rows, s.cols), s.cols, dgamma, dbeta);
 }
 
