@@ -9,11 +9,15 @@
 // bound by HBM: each row is read once into registers and used from there.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "ptx.cuh"
 #include "w2v_internal.h"
 
 namespace w2v {
 namespace {
+
+constexpr int kLnThreads = 256;
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
@@ -95,63 +99,106 @@ __device__ __forceinline__ float4 load4(const float* p, int lane, int cols, int 
   return r;
 }
 
+// Asynchronous copy of one chunk to this thread's own place in shared memory, and
+// the wait for all but the newest N rows of them: no other thread is involved.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  if (BYTES < 8) return;  // (rows of single elements are not copied this way)
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// This thread's chunks of a row from its place in a stage, kLnThreads chunks apart.
+template <typename T, int V, int NCH, int G>
+__device__ __forceinline__ void read_ring(const Vec<T, V>* slot, int lane, int cols, float2 (&out)[NCH * V / 2]) {
+  Vec<T, V> u[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    if ((lane + G * i) * V < cols) {
+      u[i] = slot[i * kLnThreads];
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) u[i].v[k] = from_f32<T>(0.f);
+    }
+  }
+  widen<T, V, NCH>(u, out);
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// Pairs of elements in packed fp32 instructions: with scalar ones both GELU passes
-// over 51199 x 512 were bound by instruction issue.
-//
-// h = Phi(-|z|) and e = exp(-z^2 / 2) for the exact GELU and its slope, which share
-// one exponential: erfc by formula 7.1.26 of Abramowitz and Stegun's Handbook
-// (Hastings), a polynomial in 1 / (1 + p x) times e, absolute error below 0.75e-7
-// in Phi.
-__device__ __forceinline__ float2 normal_tail(float2 z, float2 x, float2* e) {
-  const float2 d = ffma2(x, both(0.3275911f * 0.70710678118654752f), both(1.0f));
-  const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
-  const float2 a = fmul2(fmul2(z, both(-0.5f * 1.4426950408889634f)), z);
-  *e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-  float2 p = ffma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
-  p = ffma2(p, t, both(0.5f * 1.421413741f));
-  p = ffma2(p, t, both(0.5f * -0.284496736f));
-  p = ffma2(p, t, both(0.5f * 0.254829592f));
-  return fmul2(fmul2(p, t), *e);
+// A constant for both elements of a pair, held in registers: a packed instruction
+// takes no immediates, and left to itself the compiler moves each constant into a
+// pair of registers before each use.
+__device__ __forceinline__ float2 held(float v) {
+  float2 r;
+  asm("mov.f32 %0, %2;\n\tmov.f32 %1, %2;" : "=f"(r.x), "=f"(r.y) : "f"(v));
+  return r;
 }
 
-// The tanh form is z sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3): the sigmoid.
-__device__ __forceinline__ float2 tanh_gate(float2 z, float2 z2) {
-  constexpr float k = -2.0f * 0.7978845608028654f * 1.4426950408889634f;
-  const float2 a = fmul2(z, ffma2(z2, both(0.044715f * k), both(k)));
-  const float2 d = fadd2(make_float2(ex2_approx(a.x), ex2_approx(a.y)), both(1.0f));
-  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
-}
-
-// GELU: z Phi(z) = max(z, 0) - |z| Phi(-|z|).
+// GELU f and its slope f' on pairs of elements in packed fp32 instructions (with
+// scalar ones both passes over 51199 x 512 were bound by instruction issue).
 template <int ACT>
-__device__ __forceinline__ float2 gelu_value(float2 z) {
-  if (ACT == 1) {
-    const float2 x = make_float2(fabsf(z.x), fabsf(z.y));
-    float2 e;
-    const float2 h = normal_tail(z, x, &e);
-    return ffma2(make_float2(-x.x, -x.y), h, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
-  }
-  if (ACT == 2) return fmul2(z, tanh_gate(z, fmul2(z, z)));
-  return z;
-}
+struct Gelu {
+  __device__ __forceinline__ float2 value(float2 z) const { return z; }
+  __device__ __forceinline__ float2 slope(float2) const { return both(1.0f); }
+};
 
-// f'(z): Phi(z) + z phi(z), or s + z s (1 - s) 2 u'(z) with s = sigmoid(2u).
-template <int ACT>
-__device__ __forceinline__ float2 gelu_slope(float2 z) {
-  if (ACT == 1) {
-    float2 e;
-    const float2 h = normal_tail(z, make_float2(fabsf(z.x), fabsf(z.y)), &e);
-    const float2 q = ffma2(h, both(-1.0f), both(0.5f));
-    const float2 phi = fadd2(make_float2(copysignf(q.x, z.x), copysignf(q.y, z.y)), both(0.5f));
-    return ffma2(fmul2(z, both(0.3989422804014327f)), e, phi);
+// Exact form.  h = Phi(-|z|) and e = exp(-z^2 / 2) share one exponential: erfc by
+// formula 7.1.26 of Abramowitz and Stegun's Handbook (Hastings), a polynomial in
+// 1 / (1 + p x) times e, absolute error below 0.75e-7 in Phi.
+template <>
+struct Gelu<1> {
+  float2 a = held(-0.5f * 1.4426950408889634f);
+  float2 c5 = held(0.5f * 1.061405429f), c4 = held(0.5f * -1.453152027f), c3 = held(0.5f * 1.421413741f);
+  float2 c2 = held(0.5f * -0.284496736f), c1 = held(0.5f * 0.254829592f);
+  __device__ __forceinline__ float2 tail(float2 z, float2* e) const {
+    constexpr float p = 0.3275911f * 0.70710678118654752f;
+    const float2 t = make_float2(rcp_approx(fmaf(fabsf(z.x), p, 1.0f)), rcp_approx(fmaf(fabsf(z.y), p, 1.0f)));
+    const float2 w = fmul2(fmul2(z, a), z);
+    *e = make_float2(ex2_approx(w.x), ex2_approx(w.y));
+    const float2 te = fmul2(t, *e);
+    return fmul2(ffma2(ffma2(ffma2(ffma2(t, c5, c4), t, c3), t, c2), t, c1), te);
   }
-  constexpr float k = 0.7978845608028654f;
-  const float2 z2 = fmul2(z, z), s = tanh_gate(z, z2);
-  const float2 r = fmul2(fmul2(z, s), ffma2(s, both(-1.0f), both(1.0f)));
-  return ffma2(r, ffma2(z2, both(6.0f * 0.044715f * k), both(2.0f * k)), s);
-}
+  // z Phi(z) = max(z, 0) - |z| Phi(-|z|)
+  __device__ __forceinline__ float2 value(float2 z) const {
+    float2 e;
+    const float2 h = tail(z, &e);
+    return make_float2(fmaf(-fabsf(z.x), h.x, fmaxf(z.x, 0.f)), fmaf(-fabsf(z.y), h.y, fmaxf(z.y, 0.f)));
+  }
+  // Phi(z) + z phi(z)
+  __device__ __forceinline__ float2 slope(float2 z) const {
+    float2 e;
+    const float2 h = tail(z, &e);
+    const float2 ze = fmul2(z, e);
+    return make_float2(fmaf(0.3989422804014327f, ze.x, z.x < 0.f ? h.x : 1.0f - h.x),
+                       fmaf(0.3989422804014327f, ze.y, z.y < 0.f ? h.y : 1.0f - h.y));
+  }
+};
+
+// Tanh form: z s with s = sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3).
+template <>
+struct Gelu<2> {
+  static constexpr float k = 0.7978845608028654f, kl = -2.0f * k * 1.4426950408889634f;
+  float2 one = held(1.0f), k1 = held(kl), k3 = held(0.044715f * kl);
+  __device__ __forceinline__ float2 gate(float2 z, float2 z2) const {
+    const float2 w = fmul2(z, ffma2(z2, k3, k1));
+    const float2 d = fadd2(make_float2(ex2_approx(w.x), ex2_approx(w.y)), one);
+    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  }
+  __device__ __forceinline__ float2 value(float2 z) const { return fmul2(z, gate(z, fmul2(z, z))); }
+  // s + z s (1 - s) 2 u'(z)
+  __device__ __forceinline__ float2 slope(float2 z) const {
+    const float2 z2 = fmul2(z, z), s = gate(z, z2);
+    const float2 zs = fmul2(z, s);
+    return make_float2(fmaf(fmaf(-zs.x, s.x, zs.x), fmaf(6.0f * 0.044715f * k, z2.x, 2.0f * k), s.x),
+                       fmaf(fmaf(-zs.y, s.y, zs.y), fmaf(6.0f * 0.044715f * k, z2.y, 2.0f * k), s.y));
+  }
+};
 
 // fn(std::integral_constant<int, act>()), so that the choice is made once a row.
 template <typename F>
@@ -179,8 +226,6 @@ __device__ __forceinline__ float group_sum(float v, float* red) {
   return s;
 }
 
-constexpr int kLnThreads = 256;
-
 // Chunks a thread is given at a time: its 1 to 4 steps cover a row with at most the
 // last step's chunks past the end.
 template <typename X>
@@ -188,70 +233,108 @@ __host__ __device__ constexpr int chunk_step() {
   return sizeof(X) == 4 ? 2 : 1;
 }
 
-// G threads a row, each with NCH chunks of V elements.
-template <typename X, typename Y, int V, int NCH, int G>
+// G threads a row, each with NCH chunks of V elements; a group takes ROWS rows at
+// once (two where there are rows enough: a warp with one 1 KB row in flight reaches
+// 4.4 TB/s of the 6.5).
+template <typename X, typename Y, int V, int NCH, int G, int ROWS>
 __global__ void __launch_bounds__(kLnThreads)
 layernorm_fwd_kernel(const X* __restrict__ x, int64_t x_ld, Y* __restrict__ y, int64_t y_ld, int64_t rows, int cols,
                      const float* __restrict__ gamma, const float* __restrict__ beta, float eps, int act,
                      float* __restrict__ mean_out, float* __restrict__ rstd_out) {
   __shared__ float red[kLnThreads / 32];
   if (threadIdx.x == 0) pdl_launch_dependents();
+  constexpr int NP = NCH * V / 2;
   const int lane = threadIdx.x % G;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kLnThreads / G) + threadIdx.x / G;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * (kLnThreads / G) + threadIdx.x / G) * ROWS;
   pdl_wait();
   if (row >= rows) return;  // whole groups
-  constexpr int NP = NCH * V / 2;
-  Vec<X, V> raw[NCH];
-  load_row<X, V, NCH, G>(x + row * x_ld, lane, cols, raw);
-  float2 v[NP];
-  widen<X, V, NCH>(raw, v);
-  float2 s = v[0];
+  const int here = ROWS == 1 || row + 1 < rows ? ROWS : 1;
+  float2 v[ROWS][NP];
+  float mean[ROWS], rstd[ROWS];
+  {
+    Vec<X, V> raw[ROWS][NCH];
 #pragma unroll
-  for (int i = 1; i < NP; ++i) s = fadd2(s, v[i]);
+    for (int k = 0; k < ROWS; ++k)  // (past the last row: the last row again, not written)
+      load_row<X, V, NCH, G>(x + (row + min(k, here - 1)) * x_ld, lane, cols, raw[k]);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) widen<X, V, NCH>(raw[k], v[k]);
+  }
   const float inv = 1.0f / cols;
-  const float mean = group_sum<G>(s.x + s.y, red) * inv;
-  float2 q = both(0.f);
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    v[i] = fadd2(v[i], both(-mean));
-    // columns past the end, which can only be in the last chunks (see by_chunks)
-    const int e = 2 * i;
-    if (V == 1 || e / V >= NCH - chunk_step<X>()) {
-      if ((lane + G * (e / V)) * V >= cols) v[i].x = 0.f;
-      if ((lane + G * ((e + 1) / V)) * V >= cols) v[i].y = 0.f;
+  for (int k = 0; k < ROWS; ++k) {
+    float2 s = v[k][0];
+#pragma unroll
+    for (int i = 1; i < NP; ++i) s = fadd2(s, v[k][i]);
+    mean[k] = s.x + s.y;
+  }
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) mean[k] = group_sum<G>(mean[k], red) * inv;
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    float2 q = both(0.f);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      v[k][i] = fadd2(v[k][i], both(-mean[k]));
+      // columns past the end, which can only be in the last chunks (see by_chunks)
+      const int e = 2 * i;
+      if (V == 1 || e / V >= NCH - chunk_step<X>()) {
+        if ((lane + G * (e / V)) * V >= cols) v[k][i].x = 0.f;
+        if ((lane + G * ((e + 1) / V)) * V >= cols) v[k][i].y = 0.f;
+      }
+      q = ffma2(v[k][i], v[k][i], q);
     }
-    q = ffma2(v[i], v[i], q);
+    rstd[k] = q.x + q.y;
   }
-  const float var = group_sum<G>(q.x + q.y, red) * inv;
-  const float rstd = 1.0f / sqrtf(var + eps);
-  if (lane == 0) {
-    mean_out[row] = mean;
-    rstd_out[row] = rstd;
-  }
-  Vec<float, V> gv[NCH], bv[NCH];
-  load_row<float, V, NCH, G>(gamma, lane, cols, gv);
-  load_row<float, V, NCH, G>(beta, lane, cols, bv);
-  float2 g[NP], b[NP];
-  widen<float, V, NCH>(gv, g);
-  widen<float, V, NCH>(bv, b);
-  by_act(act, [&](auto a) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) v[i] = gelu_value<decltype(a)::value>(ffma2(fmul2(v[i], both(rstd)), g[i], b[i]));
+  for (int k = 0; k < ROWS; ++k) rstd[k] = rsqrtf(group_sum<G>(rstd[k], red) * inv + eps);
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    if (lane == 0 && k < here) {
+      mean_out[row + k] = mean[k];
+      rstd_out[row + k] = rstd[k];
+    }
+  }
+  by_act(act, [&](auto a) {
+    const Gelu<decltype(a)::value> gelu;
+#pragma unroll
+    for (int e = 0; e < 2 * NP; e += 4) {
+      const float4 g = load4<V, G>(gamma, lane, cols, e), b = load4<V, G>(beta, lane, cols, e);
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k) {
+        const float2 r = both(rstd[k]);
+        v[k][e / 2] = gelu.value(ffma2(fmul2(v[k][e / 2], r), make_float2(g.x, g.y), make_float2(b.x, b.y)));
+        v[k][e / 2 + 1] = gelu.value(ffma2(fmul2(v[k][e / 2 + 1], r), make_float2(g.z, g.w), make_float2(b.z, b.w)));
+      }
+    }
   });
-  store_row<Y, V, NCH, G>(y + row * y_ld, lane, cols, v);
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k)
+    if (k < here) store_row<Y, V, NCH, G>(y + (row + k) * y_ld, lane, cols, v[k]);
+}
+
+// Rows on their way per thread in the backward pass (see its ring).
+template <typename X, int V, int NCH>
+__host__ __device__ constexpr int bwd_stages() {
+  return V == 1 ? 0 : (sizeof(X) == 2 && NCH * V <= 16 ? 3 : 2);
+}
+template <typename X, typename Y, int V, int NCH>
+__host__ __device__ constexpr int bwd_stage_bytes(bool res) {
+  return kLnThreads * NCH * V * static_cast<int>((res ? 2 : 1) * sizeof(X) + sizeof(Y));
 }
 
 // Persistent blocks: each thread keeps its columns' dgamma and dbeta over all
-// the rows it sees, with the next row's elements on their way while one is worked
-// on; the block adds its groups' sums in order and leaves one partial per block,
-// which layernorm_affine_kernel adds up in block order.
+// the rows it sees; the block adds its groups' sums in order and leaves one
+// partial per block, which layernorm_affine_kernel adds up in block order.  The
+// next two or three rows are on their way to a ring in shared memory, every
+// thread copying what it will read (in registers there is room for one, and 16
+// warps with one row in flight each left HBM at half its rate).
 template <typename X, typename Y, int V, int NCH, int G>
 __global__ void __launch_bounds__(kLnThreads, NCH * V <= 16 ? 2 : 1)
 layernorm_bwd_kernel(const Y* __restrict__ dy, int64_t dy_ld, const X* __restrict__ x, int64_t x_ld, int64_t rows,
                      int cols, const float* __restrict__ gamma, const float* __restrict__ beta,
                      const float* __restrict__ mean, const float* __restrict__ rstd, int act, const X* dres,
                      int64_t dres_ld, X* dx, int64_t dx_ld, float* __restrict__ partial) {
-  extern __shared__ float acc[];  // [groups][2][cols] when several groups share the block
+  extern __shared__ __align__(16) uint8_t ring[];  // [stages]{x, dy, dres}; at the end [groups][2][cols] sums
   __shared__ float red[kLnThreads / 32];
   if (threadIdx.x == 0) pdl_launch_dependents();
   constexpr int kGroups = kLnThreads / G;
@@ -261,29 +344,64 @@ layernorm_bwd_kernel(const Y* __restrict__ dy, int64_t dy_ld, const X* __restric
 #pragma unroll
   for (int i = 0; i < NP; ++i) dg[i] = db[i] = both(0.f);
   const float inv = 1.0f / cols;
-  Vec<X, V> xn[NCH];
-  Vec<Y, V> yn[NCH];
-  float mn = 0.f, rn = 0.f;
-  auto fetch = [&](int64_t row) {
-    mn = mean[row];
-    rn = rstd[row];
-    load_row<X, V, NCH, G>(x + row * x_ld, lane, cols, xn);
-    load_row<Y, V, NCH, G>(dy + row * dy_ld, lane, cols, yn);
+  constexpr int kStages = bwd_stages<X, V, NCH>();
+  const int stage_bytes = bwd_stage_bytes<X, Y, V, NCH>(dres != nullptr);
+  constexpr int kXBytes = kLnThreads * NCH * V * static_cast<int>(sizeof(X));
+  constexpr int kYBytes = kLnThreads * NCH * V * static_cast<int>(sizeof(Y));
+  auto slot_x = [&](int st) { return reinterpret_cast<Vec<X, V>*>(ring + st * stage_bytes) + threadIdx.x; };
+  auto slot_y = [&](int st) { return reinterpret_cast<Vec<Y, V>*>(ring + st * stage_bytes + kXBytes) + threadIdx.x; };
+  auto slot_r = [&](int st) {
+    return reinterpret_cast<Vec<X, V>*>(ring + st * stage_bytes + kXBytes + kYBytes) + threadIdx.x;
+  };
+  auto fetch = [&](int64_t row, int st) {
+    if (row < rows) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        const int c = (lane + G * i) * V;
+        if (c < cols) {
+          copy_async<V * sizeof(X)>(slot_x(st) + i * kLnThreads, x + row * x_ld + c);
+          copy_async<V * sizeof(Y)>(slot_y(st) + i * kLnThreads, dy + row * dy_ld + c);
+          if (dres) copy_async<V * sizeof(X)>(slot_r(st) + i * kLnThreads, dres + row * dres_ld + c);
+        }
+      }
+    }
+    copy_commit();  // a group per row, an empty one past the end
   };
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
   int64_t row = static_cast<int64_t>(blockIdx.x) * kGroups + group;
   pdl_wait();
-  if (row < rows) fetch(row);
+  if (kStages > 0) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) fetch(row + i * step, i);
+  }
+  int st = 0;
+  float mn = row < rows ? mean[row] : 0.f, rn = row < rows ? rstd[row] : 0.f;
   for (; row < rows; row += step) {
     const float r = rn, m = mn;
-    float2 xh[NP], w[NP];
-    widen<X, V, NCH>(xn, xh);
-    widen<Y, V, NCH>(yn, w);
-    if (row + step < rows) fetch(row + step);
+    if (row + step < rows) {
+      mn = mean[row + step];
+      rn = rstd[row + step];
+    }
+    float2 xh[NP], w[NP], res[NP];
+    if (kStages > 0) {
+      copy_wait<kStages == 0 ? 0 : kStages - 1>();
+      read_ring<X, V, NCH, G>(slot_x(st), lane, cols, xh);
+      read_ring<Y, V, NCH, G>(slot_y(st), lane, cols, w);
+      // (dres is read when it is needed; its stage is refilled after that)
+      if (!dres) fetch(row + kStages * step, st);
+    } else {
+      Vec<X, V> xv[NCH];
+      Vec<Y, V> yv[NCH];
+      load_row<X, V, NCH, G>(x + row * x_ld, lane, cols, xv);
+      load_row<Y, V, NCH, G>(dy + row * dy_ld, lane, cols, yv);
+      widen<X, V, NCH>(xv, xh);
+      widen<Y, V, NCH>(yv, w);
+    }
     float2 s1 = both(0.f), s2 = both(0.f);
     // (columns past the end: dy is 0, so they add nothing)
     by_act(act, [&](auto a) {
       constexpr int ACT = decltype(a)::value;
+      const Gelu<ACT> gelu;
 #pragma unroll
       for (int e = 0; e < 2 * NP; e += 4) {
         const float4 g4 = load4<V, G>(gamma, lane, cols, e);
@@ -294,7 +412,7 @@ layernorm_bwd_kernel(const Y* __restrict__ dy, int64_t dy_ld, const X* __restric
           const float2 g = i & 1 ? make_float2(g4.z, g4.w) : make_float2(g4.x, g4.y);
           const float2 b = i & 1 ? make_float2(b4.z, b4.w) : make_float2(b4.x, b4.y);
           xh[i] = fmul2(fadd2(xh[i], both(-m)), both(r));
-          if (ACT != 0) w[i] = fmul2(w[i], gelu_slope<ACT>(ffma2(xh[i], g, b)));
+          if (ACT != 0) w[i] = fmul2(w[i], gelu.slope(ffma2(xh[i], g, b)));
           dg[i] = ffma2(w[i], xh[i], dg[i]);
           db[i] = fadd2(db[i], w[i]);
           w[i] = fmul2(w[i], g);
@@ -306,10 +424,14 @@ layernorm_bwd_kernel(const Y* __restrict__ dy, int64_t dy_ld, const X* __restric
     const float c1 = group_sum<G>(s1.x + s1.y, red) * inv;
     const float c2 = group_sum<G>(s2.x + s2.y, red) * inv;
     if (dres) {
-      Vec<X, V> rv[NCH];
-      load_row<X, V, NCH, G>(dres + row * dres_ld, lane, cols, rv);
-      float2 res[NP];
-      widen<X, V, NCH>(rv, res);
+      if (kStages > 0) {
+        read_ring<X, V, NCH, G>(slot_r(st), lane, cols, res);
+        fetch(row + kStages * step, st);
+      } else {
+        Vec<X, V> rv[NCH];
+        load_row<X, V, NCH, G>(dres + row * dres_ld, lane, cols, rv);
+        widen<X, V, NCH>(rv, res);
+      }
 #pragma unroll
       for (int i = 0; i < NP; ++i)
         w[i] = ffma2(both(r), ffma2(xh[i], both(-c2), fadd2(w[i], both(-c1))), res[i]);
@@ -317,10 +439,13 @@ layernorm_bwd_kernel(const Y* __restrict__ dy, int64_t dy_ld, const X* __restric
 #pragma unroll
       for (int i = 0; i < NP; ++i) w[i] = fmul2(both(r), ffma2(xh[i], both(-c2), fadd2(w[i], both(-c1))));
     }
+    st = st + 1 == kStages ? 0 : st + 1;
     store_row<X, V, NCH, G>(dx + row * dx_ld, lane, cols, w);
   }
   float* mine = partial + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+  float* acc = reinterpret_cast<float*>(ring);
   float* sums = kGroups > 1 ? acc + group * 2 * cols : mine;
+  if (kGroups > 1) __syncthreads();  // every group is done with the ring
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = (lane + G * i) * V;
@@ -400,17 +525,28 @@ int bwd_blocks(int64_t rows, int cols) {
   return static_cast<int>(want < most ? (want < 1 ? 1 : want) : most);
 }
 
+template <typename X, typename Y, int V, int NCH, int G>
+cudaError_t fwd_launch(const LnTrain& s, const void* xp, void* yp, float eps, float* mean, float* rstd,
+                       cudaStream_t st) {
+  constexpr int kPer = kLnThreads / G;
+  // Two 16-bit rows of up to 512 columns to a warp once a row each fills the GPU
+  // twice: LN2A.
+  constexpr int kRows = G == 32 && V == 8 && NCH <= 2 ? 2 : 1;
+  const bool more = kRows == 2 && s.rows >= 2 * 4 * kPer * kNumSMs;
+  const int64_t per = more ? kRows * kPer : kPer;
+  return launch_pdl(more ? layernorm_fwd_kernel<X, Y, V, NCH, G, kRows> : layernorm_fwd_kernel<X, Y, V, NCH, G, 1>,
+                    dim3(static_cast<unsigned>((s.rows + per - 1) / per)), dim3(kLnThreads), 0, st,
+                    static_cast<const X*>(xp), s.x_ld, static_cast<Y*>(yp), s.y_ld, s.rows, s.cols, s.gamma, s.beta,
+                    eps, s.act, mean, rstd);
+}
+
 template <typename X, typename Y, int G>
 cudaError_t fwd(const LnTrain& s, const void* xp, void* yp, float eps, float* mean, float* rstd, cudaStream_t st) {
   constexpr int V = 16 / sizeof(X);
   const bool vec = s.cols % V == 0 && s.x_ld % V == 0 && s.y_ld % V == 0 && aligned(xp, 16) &&
                    aligned(yp, V * sizeof(Y)) && aligned(s.gamma, 4 * V) && aligned(s.beta, 4 * V);
-  const int64_t per = kLnThreads / G;
-  const dim3 grid(static_cast<unsigned>((s.rows + per - 1) / per));
   return by_chunks<X, G>(vec, s.cols, [&](auto v, auto nch) {
-    return launch_pdl(layernorm_fwd_kernel<X, Y, decltype(v)::value, decltype(nch)::value, G>, grid, dim3(kLnThreads),
-                      0, st, static_cast<const X*>(xp), s.x_ld, static_cast<Y*>(yp), s.y_ld, s.rows, s.cols, s.gamma,
-                      s.beta, eps, s.act, mean, rstd);
+    return fwd_launch<X, Y, decltype(v)::value, decltype(nch)::value, G>(s, xp, yp, eps, mean, rstd, st);
   });
 }
 
@@ -432,10 +568,13 @@ cudaError_t bwd(const LnTrain& s, const BwdPtrs& p, cudaStream_t st) {
   const bool vec = s.cols % V == 0 && s.x_ld % V == 0 && s.y_ld % V == 0 && p.dx_ld % V == 0 &&
                    (!p.dres || (p.dres_ld % V == 0 && aligned(p.dres, 16))) && aligned(p.x, 16) && aligned(p.dx, 16) &&
                    aligned(p.dy, V * sizeof(Y)) && aligned(s.gamma, 4 * V) && aligned(s.beta, 4 * V);
-  const size_t smem = G == 32 ? kLnThreads / 32 * 2 * static_cast<size_t>(s.cols) * sizeof(float) : 0;
+  const size_t sums = G == 32 ? kLnThreads / 32 * 2 * static_cast<size_t>(s.cols) * sizeof(float) : 0;
   return by_chunks<X, G>(vec, s.cols, [&](auto v, auto nch) {
-    auto kernel = layernorm_bwd_kernel<X, Y, decltype(v)::value, decltype(nch)::value, G>;
-    if (smem > 48 * 1024) {
+    constexpr int kV = decltype(v)::value, kN = decltype(nch)::value;
+    const size_t smem = std::max(
+        sums, static_cast<size_t>(bwd_stages<X, kV, kN>()) * bwd_stage_bytes<X, Y, kV, kN>(p.dres != nullptr));
+    auto kernel = layernorm_bwd_kernel<X, Y, kV, kN, G>;
+    if (smem > 47 * 1024) {  // with the static part, more than the 48 KB that need no asking
       const cudaError_t r =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (r != cudaSuccess) return r;
