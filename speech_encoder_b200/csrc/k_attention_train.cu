@@ -69,25 +69,68 @@ __device__ __forceinline__ int clip_frames(const int32_t* frames, int b, int T) 
   return n < 0 ? 0 : (n > T ? T : n);
 }
 
-// The clip with the rank-th most frames (ties by index), for batches small enough
-// that every CTA can afford to look: work is handed out in grid order, so with the
-// longest clips first the last CTAs to start are short ones.  All lanes of the
-// warp take part and get the same answer.
+// The work unit of a CTA: 128 rows of one clip and head.  Unit u of a ragged batch
+// is the u-th in the order longest clip first (ties by index), heads, tiles, of the
+// tiles that hold frames; after those, in the same order, the tiles of padded rows
+// alone.  CTAs start in grid order, so the last to start are short ones, and those
+// with nothing but zeros to write do not hold places among the others (they did,
+// and left half of the places empty for a third of a batch of 8 clips).  For
+// batches of up to 64 clips, whose lengths a warp can hold and compare; larger ones
+// are taken as they come.  All lanes of the warp take part and get the same answer.
+struct Unit {
+  int b, h, tile, len;
+};
 constexpr int kRankedBatch = 64;
-__device__ __forceinline__ int clip_of_rank(const int32_t* frames, int batch, int T, int rank, int lane) {
-  if (batch > kRankedBatch) return rank;
-  for (int base = 0; base < batch; base += 32) {
-    const int c = base + lane;
-    const int n = c < batch ? clip_frames(frames, c, T) : -1;
-    int r = 0;
-    for (int o = 0; o < batch; ++o) {
-      const int m = clip_frames(frames, o, T);
-      r += m > n || (m == n && o < c);
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, c < batch && r == rank);
-    if (hit) return base + __ffs(hit) - 1;
+
+// How many of all `units` have frames (all, for a batch that is taken as it comes).
+__device__ __forceinline__ int live_units(const int32_t* frames, int batch, int T, int H, int units, int lane) {
+  if (batch > kRankedBatch) return units;
+  int m = lane < batch ? (clip_frames(frames, lane, T) + 127) / 128 : 0;
+  if (lane + 32 < batch) m += (clip_frames(frames, lane + 32, T) + 127) / 128;
+  return static_cast<int>(__reduce_add_sync(0xffffffffu, m)) * H;
+}
+
+__device__ __forceinline__ Unit find_unit(const int32_t* frames, int batch, int T, int H, int tiles, int u, int lane) {
+  Unit r;
+  if (!frames || batch > kRankedBatch) {
+    r.tile = u % tiles;
+    r.h = u / tiles % H;
+    r.b = u / tiles / H;
+    r.len = frames ? clip_frames(frames, r.b, T) : T;
+    return r;
   }
-  return 0;
+  const int n0 = lane < batch ? clip_frames(frames, lane, T) : -1;
+  const int n1 = lane + 32 < batch ? clip_frames(frames, lane + 32, T) : -1;
+  int before0 = 0, before1 = 0, all = 0;  // tiles with frames of the clips before this lane's two; of all clips
+  for (int o = 0; o < batch; ++o) {
+    const int n = __shfl_sync(0xffffffffu, o < 32 ? n0 : n1, o & 31), m = (n + 127) / 128;
+    if (n > n0 || (n == n0 && o < lane)) before0 += m;
+    if (n > n1 || (n == n1 && o < lane + 32)) before1 += m;
+    all += m;
+  }
+  const bool live = u < all * H;
+  const int at = live ? u : u - all * H;
+  // (counts of padded tiles likewise: all tiles less those with frames, clips in index order)
+  if (!live) {
+    before0 = before1 = 0;
+    for (int o = 0; o < batch; ++o) {
+      const int n = __shfl_sync(0xffffffffu, o < 32 ? n0 : n1, o & 31), m = tiles - (n + 127) / 128;
+      if (o < lane) before0 += m;
+      if (o < lane + 32) before1 += m;
+    }
+  }
+  const int m0 = n0 < 0 ? 0 : (live ? (n0 + 127) / 128 : tiles - (n0 + 127) / 128);
+  const int m1 = n1 < 0 ? 0 : (live ? (n1 + 127) / 128 : tiles - (n1 + 127) / 128);
+  const bool mine0 = at >= before0 * H && at < (before0 + m0) * H;
+  const bool mine1 = at >= before1 * H && at < (before1 + m1) * H;
+  const int src = __ffs(__ballot_sync(0xffffffffu, mine0 || mine1)) - 1;
+  const int m = __shfl_sync(0xffffffffu, mine1 ? m1 : m0, src);
+  const int in = at - __shfl_sync(0xffffffffu, mine1 ? before1 : before0, src) * H;
+  r.b = __shfl_sync(0xffffffffu, mine1 ? lane + 32 : lane, src);
+  r.len = __shfl_sync(0xffffffffu, mine1 ? n1 : n0, src);
+  r.h = in / m;
+  r.tile = in % m + (live ? 0 : tiles - m);
+  return r;
 }
 
 // 2^x of a pair on the FMA and ALU pipes, for the share of the exponentials that
@@ -200,13 +243,9 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 + 2 * FwdSmem::kStages);
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int qt = blockIdx.x % tiles, h = blockIdx.x / tiles % H;
-  int b = blockIdx.x / tiles / H, len = T;
-  if (frames) {
-    pdl_wait();
-    b = clip_of_rank(frames, batch, T, b, lane);
-    len = clip_frames(frames, b, T);
-  }
+  if (frames) pdl_wait();
+  const Unit unit = find_unit(frames, batch, T, H, tiles, blockIdx.x, lane);
+  const int b = unit.b, h = unit.h, qt = unit.tile, len = unit.len;
   const int64_t bh = static_cast<int64_t>(b) * H + h;
   const int nkv = (len + kSub - 1) / kSub;
   if (qt * 128 >= len) {  // rows past the clip
@@ -616,7 +655,7 @@ struct BwdArgs {
 
 template <bool BF16, bool KEYS>
 __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensorMap& tmA2, const CUtensorMap& tmB1,
-                                         const CUtensorMap& tmB2, const BwdArgs& a, int unit) {
+                                         const CUtensorMap& tmB2, const BwdArgs& a, int u) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BwdSmem::BAR);
@@ -631,13 +670,8 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6 + 2 * BwdSmem::kStages);
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int tile = unit % a.tiles, h = unit / a.tiles % a.H;
-  int b = unit / a.tiles / a.H, len = a.T;
-  if (a.frames) {
-    pdl_wait();
-    b = clip_of_rank(a.frames, a.batch, a.T, b, lane);
-    len = clip_frames(a.frames, b, a.T);
-  }
+  const Unit unit = find_unit(a.frames, a.batch, a.T, a.H, a.tiles, u, lane);
+  const int b = unit.b, h = unit.h, tile = unit.tile, len = unit.len;
   const int64_t bh = static_cast<int64_t>(b) * a.H + h;
   const int n_sub = (len + kSub - 1) / kSub;
   if (tile * 128 >= len) {  // rows past the clip
@@ -906,12 +940,18 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
 attention_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDo,
                      const __grid_constant__ BwdArgs a) {
-  // key CTAs, the longer ones, first
+  // In this order: key CTAs (the longer ones) and query CTAs of tiles with frames,
+  // key CTAs and query CTAs of padded rows alone.
   const int units = a.tiles * a.batch * a.H, u = blockIdx.x;
-  if (u < units)
-    bwd_body<BF16, true>(tmK, tmV, tmQ, tmDo, a, u);
+  int live = units;
+  if (a.frames) {
+    pdl_wait();
+    live = live_units(a.frames, a.batch, a.T, a.H, units, threadIdx.x & 31);
+  }
+  if (u < live || (u >= 2 * live && u < units + live))
+    bwd_body<BF16, true>(tmK, tmV, tmQ, tmDo, a, u < live ? u : u - live);
   else
-    bwd_body<BF16, false>(tmQ, tmDo, tmK, tmV, a, u - units);
+    bwd_body<BF16, false>(tmQ, tmDo, tmK, tmV, a, u < 2 * live ? u - live : u - units);
 }
 
 // [batch][T][H][64] operand as {H * 64, T, batch}, 64-row boxes of one head.

@@ -469,28 +469,33 @@ layernorm_bwd_kernel(const Y* __restrict__ dy, int64_t dy_ld, const X* __restric
   }
 }
 
-// dgamma and dbeta: the blocks' partials added in a fixed order.  A block takes 32
-// columns of the 2 cols; 16 warps add every 16th partial, then warp 0 the 16.
-constexpr int kAffineWarps = 16;
-__global__ void __launch_bounds__(32 * kAffineWarps)
+// dgamma and dbeta: the blocks' partials added in a fixed order.  A block takes 8
+// columns of the 2 cols with 64 threads each, so that all of a thread's loads (5
+// of 296 partials) are in flight at once; 32 columns to a block with 16 warps took
+// 7 us for 1024 columns where this takes LNC.
+constexpr int kAffineCols = 8, kAffineThreads = 512;
+__global__ void __launch_bounds__(kAffineThreads)
 layernorm_affine_kernel(const float* __restrict__ partial, int blocks, int cols, float* __restrict__ dgamma,
                         float* __restrict__ dbeta) {
-  __shared__ float red[kAffineWarps][32];
+  __shared__ float red[kAffineThreads / 32][kAffineCols];
   if (threadIdx.x == 0) pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x * 32 + lane;
+  const int col = threadIdx.x % kAffineCols;
+  const int c = blockIdx.x * kAffineCols + col;
   pdl_wait();
   float s = 0.f;
   if (c < 2 * cols) {
 #pragma unroll 8
-    for (int i = warp; i < blocks; i += kAffineWarps) s += partial[static_cast<int64_t>(i) * 2 * cols + c];
+    for (int i = threadIdx.x / kAffineCols; i < blocks; i += kAffineThreads / kAffineCols)
+      s += partial[static_cast<int64_t>(i) * 2 * cols + c];
   }
-  red[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < 2 * cols) {
-    s = red[0][lane];
 #pragma unroll
-    for (int i = 1; i < kAffineWarps; ++i) s += red[i][lane];
+  for (int o = kAffineCols; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (threadIdx.x % 32 < kAffineCols) red[threadIdx.x / 32][col] = s;
+  __syncthreads();
+  if (threadIdx.x < kAffineCols && c < 2 * cols) {
+    s = red[0][col];
+#pragma unroll
+    for (int i = 1; i < kAffineThreads / 32; ++i) s += red[i][col];
     (c < cols ? dgamma + c : dbeta + (c - cols))[0] = s;
   }
 }
@@ -532,7 +537,7 @@ cudaError_t fwd_launch(const LnTrain& s, const void* xp, void* yp, float eps, fl
   // Two 16-bit rows of up to 512 columns to a warp once a row each fills the GPU
   // twice: LN2A.
   constexpr int kRows = G == 32 && V == 8 && NCH <= 2 ? 2 : 1;
-  const bool more = kRows == 2 && s.rows >= 2 * 4 * kPer * kNumSMs;
+  const bool more = kRows == 2 && s.rows >= 2 * kPer * kNumSMs;
   const int64_t per = more ? kRows * kPer : kPer;
   return launch_pdl(more ? layernorm_fwd_kernel<X, Y, V, NCH, G, kRows> : layernorm_fwd_kernel<X, Y, V, NCH, G, 1>,
                     dim3(static_cast<unsigned>((s.rows + per - 1) / per)), dim3(kLnThreads), 0, st,
@@ -622,7 +627,8 @@ cudaError_t launch_layernorm_bwd(const LnTrain& s, const void* dy, const void* x
     return s.cols <= kWarpCols ? bwd<X, Y, 32>(s, p, st) : bwd<X, Y, kLnThreads>(s, p, st);
   });
   if (r != cudaSuccess) return r;
-  return launch_pdl(layernorm_affine_kernel, dim3((2 * s.cols + 31) / 32), dim3(32 * kAffineWarps), 0, st, p.partial,
+  return launch_pdl(layernorm_affine_kernel, dim3((2 * s.cols + kAffineCols - 1) / kAffineCols),
+                    dim3(kAffineThreads), 0, st, p.partial,
                     bwd_blocks(s.rows, s.cols), s.cols, dgamma, dbeta);
 }
 
