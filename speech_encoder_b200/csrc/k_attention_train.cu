@@ -503,20 +503,38 @@ __device__ __forceinline__ uint4 aug_pieces(float v, bool rowsum, int half) {
                     pack2<BF16>(ch[6], ch[7]));
 }
 
-// In fp16 also, per 128 frames, the largest |dout row|^2 and |v row|^2.
+struct BwdOut {
+  uint16_t* dq;
+  uint16_t* dk;
+  uint16_t* dv;
+  int64_t ld, bs;
+};
+
+// In fp16 also, per 128 frames, the largest |dout row|^2 and |v row|^2.  Tiles of
+// padded rows alone get their zero gradients here.
 // Eight lanes a row, 16 bytes each.
 template <bool BF16>
 __global__ void __launch_bounds__(256)
 attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ out, int64_t out_ld,
                           int64_t out_bs, const uint16_t* __restrict__ v, int64_t v_ld, int64_t v_bs,
                           const float* __restrict__ lse, const int32_t* __restrict__ frames, int T, int H, int tiles,
-                          uint8_t* __restrict__ aug_l, uint8_t* __restrict__ aug_d, float2* __restrict__ peak) {
+                          uint8_t* __restrict__ aug_l, uint8_t* __restrict__ aug_d, float2* __restrict__ peak,
+                          const BwdOut g) {
   if (threadIdx.x == 0) pdl_launch_dependents();
   const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
   const int b = bh / H, h = bh % H;
   const int part = threadIdx.x & 7;
   pdl_wait();
   const int len = clip_frames(frames, b, T);
+  if (tile * 128 >= len) {  // rows past the clip: their gradients are written here, the rest is not asked for
+    const int to = min(T, tile * 128 + 128);
+    const int64_t at = b * g.bs + h * kHd;
+    zero_rows(g.dq + at, g.ld, tile * 128, to);
+    zero_rows(g.dk + at, g.ld, tile * 128, to);
+    zero_rows(g.dv + at, g.ld, tile * 128, to);
+    if (!BF16 && threadIdx.x == 0) peak[static_cast<int64_t>(bh) * tiles + tile] = make_float2(0.f, 0.f);
+    return;
+  }
   float top_do = 0.f, top_v = 0.f;
   // every load of the thread's four rows before any arithmetic
   uint4 ra[4], ro[4], rv[4];
@@ -641,10 +659,7 @@ struct BwdSmem {
 constexpr int kBwdThreads = 320;
 
 struct BwdArgs {
-  uint16_t* dq;
-  uint16_t* dk;
-  uint16_t* dv;
-  int64_t grad_ld, grad_bs;
+  BwdOut g;
   const int32_t* frames;
   const uint8_t* aug_l;
   const uint8_t* aug_d;
@@ -674,12 +689,8 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
   const int b = unit.b, h = unit.h, tile = unit.tile, len = unit.len;
   const int64_t bh = static_cast<int64_t>(b) * a.H + h;
   const int n_sub = (len + kSub - 1) / kSub;
-  if (tile * 128 >= len) {  // rows past the clip
+  if (tile * 128 >= len) {  // padded rows, in a batch that is taken as it comes
     if (threadIdx.x == 0) pdl_launch_dependents();
-    const int to = min(a.T, tile * 128 + 128);
-    const int64_t at = b * a.grad_bs + h * kHd;
-    zero_rows((KEYS ? a.dk : a.dq) + at, a.grad_ld, tile * 128, to);
-    if (KEYS) zero_rows(a.dv + at, a.grad_ld, tile * 128, to);
     return;
   }
 
@@ -922,9 +933,9 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
     }
     named_barrier_sync(1, 256);
     const int rows = min(128, a.T - tile * 128);
-    const int64_t at = b * a.grad_bs + static_cast<int64_t>(tile) * 128 * a.grad_ld + h * kHd;
-    store_tile(smem + BwdSmem::A, (KEYS ? a.dk : a.dq) + at, a.grad_ld, rows, threadIdx.x, 256);
-    if (KEYS) store_tile(smem + BwdSmem::A + 2 * kTileBytes, a.dv + at, a.grad_ld, rows, threadIdx.x, 256);
+    const int64_t at = b * a.g.bs + static_cast<int64_t>(tile) * 128 * a.g.ld + h * kHd;
+    store_tile(smem + BwdSmem::A, (KEYS ? a.g.dk : a.g.dq) + at, a.g.ld, rows, threadIdx.x, 256);
+    if (KEYS) store_tile(smem + BwdSmem::A + 2 * kTileBytes, a.g.dv + at, a.g.ld, rows, threadIdx.x, 256);
   }
 
   tc_fence_before();
@@ -941,17 +952,18 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDo,
                      const __grid_constant__ BwdArgs a) {
   // In this order: key CTAs (the longer ones) and query CTAs of tiles with frames,
-  // key CTAs and query CTAs of padded rows alone.
-  const int units = a.tiles * a.batch * a.H, u = blockIdx.x;
-  int live = units;
+  // and CTAs with nothing to do (the grid is for full clips).
+  int live = a.tiles * a.batch * a.H;
   if (a.frames) {
     pdl_wait();
-    live = live_units(a.frames, a.batch, a.T, a.H, units, threadIdx.x & 31);
+    live = live_units(a.frames, a.batch, a.T, a.H, live, threadIdx.x & 31);
   }
-  if (u < live || (u >= 2 * live && u < units + live))
-    bwd_body<BF16, true>(tmK, tmV, tmQ, tmDo, a, u < live ? u : u - live);
+  const int u = blockIdx.x;
+  if (u >= 2 * live) return;
+  if (u < live)
+    bwd_body<BF16, true>(tmK, tmV, tmQ, tmDo, a, u);
   else
-    bwd_body<BF16, false>(tmQ, tmDo, tmK, tmV, a, u < 2 * live ? u - live : u - units);
+    bwd_body<BF16, false>(tmQ, tmDo, tmK, tmV, a, u - live);
 }
 
 // [batch][T][H][64] operand as {H * 64, T, batch}, 64-row boxes of one head.
@@ -1000,15 +1012,12 @@ cudaError_t launch_attention_bwd(const AttnTrain& s, const void* dout, const voi
   uint8_t* aug_d = aug_l + rows * kAugRow;
   float2* peak = reinterpret_cast<float2*>(aug_d + rows * kAugRow);
   auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
+  BwdArgs a;
+  a.g = {static_cast<uint16_t*>(dq), static_cast<uint16_t*>(dk), static_cast<uint16_t*>(dv), s.grad_ld, s.grad_bs};
   r = launch_pdl(s.bf16 ? attention_bwd_rows_kernel<true> : attention_bwd_rows_kernel<false>, dim3(tiles * bh),
                  dim3(256), 0, st, u16(dout), u16(out), s.out_ld, s.out_bs, u16(v), s.qkv_ld, s.qkv_bs, lse, s.frames,
-                 s.T, s.H, tiles, aug_l, aug_d, peak);
+                 s.T, s.H, tiles, aug_l, aug_d, peak, a.g);
   if (r != cudaSuccess) return r;
-  BwdArgs a;
-  a.dq = static_cast<uint16_t*>(dq);
-  a.dk = static_cast<uint16_t*>(dk);
-  a.dv = static_cast<uint16_t*>(dv);
-  a.grad_ld = s.grad_ld; a.grad_bs = s.grad_bs;
   a.frames = s.frames;
   a.aug_l = aug_l;
   a.aug_d = aug_d;
