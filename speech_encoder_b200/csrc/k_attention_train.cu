@@ -133,8 +133,11 @@ __device__ __forceinline__ Unit find_unit(const int32_t* frames, int batch, int 
   return r;
 }
 
-// 2^x of a pair on the FMA and ALU pipes, for the share of the exponentials that
-// the exponent unit (16 a clock per SM) has no time for: x = j + f with j the
+// 2^x of a pair on the FMA and ALU pipes, for a share of the forward pass's
+// exponentials: its softmax warps are bound by the exponent unit (16 a clock per SM)
+// and by issue about equally, and the share's optimum is flat (2 x 2999 frames x 16
+// heads: none 118 us, a quarter of the pairs 115, half 124).  The backward pass,
+// which has more else to do, is fastest with none.  x = j + f with j the
 // nearest integer (adding 1.5 * 2^23 leaves j in the low mantissa bits), 2^f by the
 // polynomial of degree 4 with the smallest largest relative error on [-1/2, 1/2]
 // (2.7e-6, found by linear programming over a fine grid), j added to the
@@ -154,12 +157,7 @@ __device__ __forceinline__ float2 exp2_poly(float2 x) {
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
-// 2^x of pair number i of a row part; POLY of every 4 pairs by polynomial.
-template <int POLY>
-__device__ __forceinline__ float2 exp2_pair(float2 x, int i) {
-  if ((i & 3) < POLY) return exp2_poly(x);
-  return make_float2(ex2_approx(x.x), ex2_approx(x.y));
-}
+__device__ __forceinline__ float2 exp2_unit(float2 x) { return make_float2(ex2_approx(x.x), ex2_approx(x.y)); }
 
 // Zeros over the 64 columns of one head in rows [from, to).
 __device__ __forceinline__ void zero_rows(uint16_t* p, int64_t ld, int from, int to) {
@@ -205,28 +203,26 @@ __device__ __forceinline__ void store_tile(const uint8_t* tile, uint16_t* dst, i
 }
 
 // -------------------------------------------------------------------- forward
-// One CTA per (128-query tile, clip and head): warps 0-3 softmax, one thread
-// per query row; warp 4 TMA; warp 5 tensor memory and products.  Within a CTA
-// the steps of a 64-key tile (scores, softmax, P V) follow one another; 128
-// tensor-memory columns and 50 KB of shared memory let four CTAs share an SM
-// and fill each other's gaps.
+// One CTA per (128-query tile, clip and head): warps 0-3 softmax, one thread per
+// query row; warp 4 TMA; warp 5 tensor memory and products.  Three score buffers of
+// 64 keys in turn: the scores of tile j + 2 are issued once P V of tile j - 1, which
+// had their buffer, is done, so the softmax warps go from tile to tile without
+// waiting for a product.  P, packed, overwrites the columns that its thread has
+// read; the accumulator is touched only when a row's reference maximum moves, after
+// the previous P V.  256 tensor-memory columns and 82 KB of shared memory: two CTAs
+// an SM (four with one score buffer each took 134 us for 2 x 2999 frames x 16 heads
+// where this takes 115).
 struct FwdSmem {
-  static constexpr int kStages = 2;
+  static constexpr int kStages = 4;
   static constexpr int Q = 0;
   static constexpr int KV = 2 * kTileBytes;  // [stages]{K, V}
   static constexpr int BAR = KV + kStages * 2 * kTileBytes;
-  static constexpr int TOTAL = BAR + 128 + 1024;
+  static constexpr int TOTAL = BAR + 256 + 1024;
 };
 constexpr int kFwdThreads = 192;
-#ifndef FWD_POLY
-#define FWD_POLY 2
-#endif
-#ifndef BWD_POLY
-#define BWD_POLY 0
-#endif
 
 template <bool BF16>
-__global__ void __launch_bounds__(kFwdThreads, 4)
+__global__ void __launch_bounds__(kFwdThreads, 2)
 attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const int32_t* __restrict__ frames, int T, int H,
                      int batch, int tiles, uint16_t* __restrict__ out, int64_t out_ld, int64_t out_bs, float* __restrict__ lse,
@@ -235,12 +231,12 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + FwdSmem::BAR);
   uint64_t* q_full = bars;
-  uint64_t* s_full = bars + 1;
-  uint64_t* p_full = bars + 2;
-  uint64_t* pv_done = bars + 3;
-  uint64_t* kv_full = bars + 4;
-  uint64_t* kv_empty = bars + 4 + FwdSmem::kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 + 2 * FwdSmem::kStages);
+  uint64_t* s_full = bars + 1;   // [3], by score buffer
+  uint64_t* p_full = bars + 4;   // [3]
+  uint64_t* pv_done = bars + 7;  // [2], by parity of the tile
+  uint64_t* kv_full = bars + 9;
+  uint64_t* kv_empty = bars + 9 + FwdSmem::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 9 + 2 * FwdSmem::kStages);
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (frames) pdl_wait();
@@ -258,9 +254,12 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(s_full, 1);
-    mbar_init(p_full, 4);
-    mbar_init(pv_done, 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+    }
+    mbar_init(&pv_done[0], 1);
+    mbar_init(&pv_done[1], 1);
     for (int i = 0; i < FwdSmem::kStages; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
@@ -269,14 +268,14 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     pdl_launch_dependents();
   }
   if (warp == 5) {
-    tmem_alloc(tmem_slot, 128);
+    tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
-  const uint32_t tS = tmem, tO = tmem + 64;
+  const uint32_t tS = tmem, tO = tmem + 192;  // scores at 0, 64, 128
   if (!frames) pdl_wait();
 
   if (warp == 4) {
@@ -309,38 +308,43 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     constexpr uint32_t idS = idesc_train<BF16>(128, kSub, false);
     constexpr uint32_t idO = idesc_train<BF16>(128, kHd, true);
     const uint64_t dQ = desc_sw128(smem_u32(smem + FwdSmem::Q));
-    bool ok = mbar_wait(q_full, 0);
-    for (int j = 0; j < nkv; ++j) {
+    const uint64_t dKV = desc_sw128(smem_u32(smem + FwdSmem::KV));
+    auto tile_k = [&](int j) { return dKV + static_cast<uint64_t>((j % FwdSmem::kStages) * (2 * kTileBytes >> 4)); };
+    auto scores = [&](int j) {
       const int st = j % FwdSmem::kStages;
-      uint8_t* kv = smem + FwdSmem::KV + st * 2 * kTileBytes;
-      // P of the previous tile lies over the scores: its product must be done.
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(&kv_full[st], (j / FwdSmem::kStages) & 1) &&
-                                       (j == 0 || mbar_wait(pv_done, (j - 1) & 1)));
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&kv_full[st], (j / FwdSmem::kStages) & 1))) return false;
       const int valid = len - j * kSub;
       if (valid < kSub) {
-        zero_tail_rows(kv + kTileBytes, valid, lane);
+        zero_tail_rows(smem + FwdSmem::KV + st * 2 * kTileBytes + kTileBytes, valid, lane);
         fence_proxy_async_smem();
+        __syncwarp();
       }
-      __syncwarp();
-      const uint64_t dK = desc_sw128(smem_u32(kv)), dV = desc_sw128(smem_u32(kv + kTileBytes));
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma_f16(tS, dQ + 2 * kk, dK + 2 * kk, idS, kk);
-        umma_commit(s_full);
+        for (int kk = 0; kk < 4; ++kk) umma_f16(tS + 64 * (j % 3), dQ + 2 * kk, tile_k(j) + 2 * kk, idS, kk);
+        umma_commit(&s_full[j % 3]);
       }
       __syncwarp();
-      ok = __all_sync(0xffffffffu, mbar_wait(p_full, j & 1));
-      if (!ok) break;
+      return true;
+    };
+    bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0)) && scores(0) && (nkv < 2 || scores(1));
+    for (int j = 0; ok && j < nkv; ++j) {
+      if (j + 2 < nkv) {
+        if (j > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1));
+        if (!ok || !(ok = scores(j + 2))) break;
+      }
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&p_full[j % 3], (j / 3) & 1)))) break;
       tc_fence_after();
       if (elect_one()) {
         // 16 keys a step: 8 packed columns of P, 16 rows (2048 bytes) of V.
+        const uint64_t dV = tile_k(j) + (kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_f16_ts(tO, tS + 8 * kk, dV + static_cast<uint64_t>(128 * kk), idO, (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&kv_empty[st]);
-        umma_commit(pv_done);
+          umma_f16_ts(tO, tS + 64 * (j % 3) + 8 * kk, dV + static_cast<uint64_t>(128 * kk), idO,
+                      (j > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&pv_done[j & 1]);
+        umma_commit(&kv_empty[j % FwdSmem::kStages]);
       }
       __syncwarp();
     }
@@ -351,70 +355,70 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     float m_ref = -INFINITY, l = 0.f;  // reference maximum (log2 units), sum of exponentials
     bool ok = true;
     for (int j = 0; j < nkv; ++j) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, j & 1));
+      const uint32_t cols = tS + 64 * (j % 3) + lane_base;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_full[j % 3], (j / 3) & 1));
       if (ok) {
         tc_fence_after();
         const int valid = len - j * kSub;
-        float s[32];
-        float mx = -INFINITY;
+        float s[kSub];
+        tmem_ld32(cols, *reinterpret_cast<float(*)[32]>(s));
+        tmem_ld32(cols + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+        if (valid < kSub) {
 #pragma unroll
-        for (int c0 = 0; c0 < kSub; c0 += 32) {
-          tmem_ld32(tS + lane_base + c0, s);
-          if (valid < kSub) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c0 + i >= valid) s[i] = -INFINITY;
-          }
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) mx = fmax3(mx, s[i], s[i + 1]);
+          for (int i = 0; i < kSub; ++i)
+            if (i >= valid) s[i] = -INFINITY;
         }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < kSub; i += 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = i + 4 < kSub ? fmax3(mx[k], s[i + k], s[i + 4 + k]) : fmaxf(mx[k], s[i + k]);
+        }
+        mx[0] = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
         // The reference moves only when the maximum exceeds it by 2^8, so the
         // accumulator is rarely rescaled and P stays <= 256.
-        const bool move = mx * kC2 > m_ref + 8.0f;
+        const bool move = mx[0] * kC2 > m_ref + 8.0f;
         if (__any_sync(0xffffffffu, move)) {
-          const float m_new = move ? mx * kC2 : m_ref;
+          const float m_new = move ? mx[0] * kC2 : m_ref;
           if (j > 0) {
-            const float alpha = ex2_approx(m_ref - m_new);
-            l *= alpha;
-            float o[16];
+            // (P V of tile j - 3 was done before these scores: the parity is the last one's)
+            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1));
+            if (ok) {
+              tc_fence_after();
+              const float alpha = ex2_approx(m_ref - m_new);
+              l *= alpha;
+              float o[16];
 #pragma unroll
-            for (int c0 = 0; c0 < kHd; c0 += 16) {
-              tmem_ld16(tO + lane_base + c0, o);
+              for (int c0 = 0; c0 < kHd; c0 += 16) {
+                tmem_ld16(tO + lane_base + c0, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= alpha;
-              tmem_st16(tO + lane_base + c0, o);
+                for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                tmem_st16(tO + lane_base + c0, o);
+              }
             }
           }
           m_ref = m_new;
         }
-        // P of each half, packed, goes over score columns that were read already:
-        // 0..15, then 16..31.
+        uint32_t pk[kSub / 2];
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c0 = 0; c0 < kSub; c0 += 32) {
-          tmem_ld32(tS + lane_base + c0, s);
-          if (valid < kSub) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c0 + i >= valid) s[i] = -INFINITY;
-          }
-          uint32_t pk[16];
-          float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 x = ffma2(make_float2(s[i], s[i + 1]), make_float2(kC2, kC2), make_float2(-m_ref, -m_ref));
-            const float2 p = exp2_pair<FWD_POLY>(x, i / 2);
-            sum = fadd2(sum, p);
-            pk[i / 2] = pack2<BF16>(p.x, p.y);
-          }
-          l += sum.x + sum.y;
-          tmem_st16_u32(tS + lane_base + c0 / 2, pk);
+        for (int i = 0; i < kSub; i += 2) {
+          const float2 x = ffma2(make_float2(s[i], s[i + 1]), make_float2(kC2, kC2), make_float2(-m_ref, -m_ref));
+          const float2 p = i % 8 == 0 ? exp2_poly(x) : exp2_unit(x);  // (a quarter, see exp2_poly)
+          sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], p);
+          pk[i / 2] = pack2<BF16>(p.x, p.y);
         }
+        sum[0] = fadd2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
+        // over the first half of the columns, which were read above
+        tmem_st16_u32(cols, *reinterpret_cast<const uint32_t(*)[16]>(pk));
+        tmem_st16_u32(cols + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      if (lane == 0) mbar_arrive(&p_full[j % 3]);
     }
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (nkv - 1) & 1));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(nkv - 1) & 1], ((nkv - 1) >> 1) & 1));
     const int t = qt * 128 + r;
     if (ok) {
       tc_fence_after();
@@ -436,7 +440,7 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   __syncthreads();
   if (warp == 5) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -875,8 +879,8 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
       if (lane == 0) mbar_arrive(s_read);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
-        const float2 p = exp2_pair<BWD_POLY>(
-            ffma2(make_float2(s[i], s[i + 1]), make_float2(kC2, kC2), make_float2(shift, shift)), i / 2);
+        const float2 p =
+            exp2_unit(ffma2(make_float2(s[i], s[i + 1]), make_float2(kC2, kC2), make_float2(shift, shift)));
         s[i] = p.x;
         s[i + 1] = p.y;
       }

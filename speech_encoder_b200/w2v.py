@@ -379,12 +379,12 @@ def _type_code(dtype) -> int:
 
 def _on_current_device(what: str, tensors):
     import torch
-    if not all(t.is_cuda for t in tensors):
-        _refuse(f"{what}: a tensor is not on the GPU")
-    cur = torch.cuda.current_device()
+    cur = tensors[0].get_device()  # -1: not on a GPU
     for t in tensors:
         if t.get_device() != cur:
-            _refuse(f"{what}: a tensor is not on the current device")
+            _refuse(f"{what}: tensors on different devices")
+    if cur < 0 or cur != torch.cuda.current_device():
+        _refuse(f"{what}: a tensor is not on the current GPU")
 
 
 def _workspace(ws, nbytes: int, device, stream):
