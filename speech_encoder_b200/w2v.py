@@ -8,7 +8,9 @@ from __future__ import annotations
 
 import array
 import ctypes
+import importlib
 import os
+import sys
 from typing import Optional
 
 import numpy as np
@@ -124,7 +126,7 @@ def _ptr(x) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
+        torch = sys.modules.get("torch") or importlib.import_module("torch")
         # the handle of torch.cuda.current_stream(), without building its Python object (3 us)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
@@ -366,30 +368,36 @@ def _refuse(what: str):
     raise W2VError(W2V_EINVAL, what)
 
 
+_TYPES: dict = {}  # torch's element types -> the library's codes
+
+
 def _type_code(dtype) -> int:
-    import torch
-    if dtype == torch.float16:
-        return 0
-    if dtype == torch.bfloat16:
-        return 1
-    if dtype != torch.float32:
-        _refuse(f"element type {dtype}")
-    return 2
+    code = _TYPES.get(dtype)
+    if code is None:
+        import torch
+        _TYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+        code = _TYPES.get(dtype)
+        if code is None:
+            _refuse(f"element type {dtype}")
+    return code
 
 
 def _on_current_device(what: str, tensors):
-    import torch
     cur = tensors[0].get_device()  # -1: not on a GPU
     for t in tensors:
         if t.get_device() != cur:
             _refuse(f"{what}: tensors on different devices")
-    if cur < 0 or cur != torch.cuda.current_device():
+    if cur < 0 or cur != _torch().cuda.current_device():
         _refuse(f"{what}: a tensor is not on the current GPU")
+
+
+def _torch():
+    return sys.modules["torch"]  # (the caller's tensors are its: no import statement, which costs more)
 
 
 def _workspace(ws, nbytes: int, device, stream):
     """The caller's workspace, or one from torch's allocator, owned by the stream that the call runs on."""
-    import torch
+    torch = _torch()
     if ws is not None:
         if not ws.is_contiguous() or ws.device != device:
             _refuse("workspace: not contiguous, or on another device")
@@ -414,8 +422,7 @@ def _row_strides(what: str, shape, tensors):
 
 
 def _attention_shape(qkv, outs, grads, lse, err, frames) -> w2v_attention_shape:
-    import torch
-    q = qkv[0]
+    torch, q = _torch(), qkv[0]
     shape, dtype = q.shape, q.dtype
     if len(shape) != 3 or shape[2] == 0 or shape[2] % 64:
         _refuse("attention: q is not [batch, T, H * 64]")
@@ -473,9 +480,9 @@ def _norm_rows(what: str, t, shape) -> int:
 
 
 def _norm_vectors(n: int, vectors):
-    import torch
+    f32 = _torch().float32
     for t in vectors:
-        if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        if t.dtype != f32 or t.numel() != n or not t.is_contiguous():
             _refuse("layernorm: a vector is not contiguous float32 of its size")
 
 
@@ -531,7 +538,7 @@ def w2v_op_grad_clip(grads, outs, scale: float, max_norm: float, norm, ws=None, 
     """norm[0] = scale * 2-norm of all grads; outs[i] = grads[i] * scale * min(1, max_norm / (norm + 1e-6)).
     grads, outs: lists of contiguous tensors (outs[i] may be grads[i]); norm: float32 [1] on the device.
     ws: a workspace of w2v_op_grad_clip_workspace bytes, or None for one from torch's allocator."""
-    import torch
+    torch = _torch()
     Tensor, n = torch.Tensor, len(grads)
     if len(outs) != n:
         _refuse("grad_clip: not as many outputs as gradients")
