@@ -46,6 +46,7 @@ int attention_args(const w2v_attention_shape* s, bool grads, AttnTrain* a) {
   a->out_ld = s->out_ld; a->out_bs = s->out_bs;
   a->grad_ld = s->grad_ld; a->grad_bs = s->grad_bs;
   a->frames = s->frames;
+  if (reinterpret_cast<uintptr_t>(s->frames) % 4 != 0) return W2V_EINVAL;
   const int64_t width = 64 * static_cast<int64_t>(s->H);
   if (!strides_ok(&a->qkv_ld, &a->qkv_bs, s->T, s->batch, width)) return W2V_EINVAL;
   if (!strides_ok(&a->out_ld, &a->out_bs, s->T, s->batch, width)) return W2V_EINVAL;
@@ -86,7 +87,9 @@ extern "C" int w2v_op_attention_fwd(const w2v_attention_shape* shape, const void
   const int rc = attention_args(shape, false, &a);
   if (rc != W2V_OK) return rc;
   if (!q || !k || !v || !out || !lse || !err_dev) return W2V_EINVAL;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned_to(lse, 4)) return W2V_EINVAL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned_to(lse, 4) ||
+      !aligned_to(err_dev, 4))
+    return W2V_EINVAL;
   return status(launch_attention_fwd(a, q, k, v, out, lse, err_dev, static_cast<cudaStream_t>(stream)));
 }
 
@@ -105,7 +108,7 @@ extern "C" int w2v_op_attention_bwd(const w2v_attention_shape* shape, const void
   for (const void* p : {dout, q, k, v, out, static_cast<const void*>(dq), static_cast<const void*>(dk),
                         static_cast<const void*>(dv), static_cast<const void*>(ws)})
     if (!aligned16(p)) return W2V_EINVAL;
-  if (!aligned_to(lse, 4)) return W2V_EINVAL;
+  if (!aligned_to(lse, 4) || !aligned_to(err_dev, 4)) return W2V_EINVAL;
   if (ws_bytes < attention_bwd_ws_bytes(a.batch, a.T, a.H)) return W2V_EINVAL;
   return status(launch_attention_bwd(a, dout, q, k, v, out, lse, dq, dk, dv, ws, err_dev,
                                      static_cast<cudaStream_t>(stream)));

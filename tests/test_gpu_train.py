@@ -105,6 +105,88 @@ def test_attention_matches_fp64(dtype, Bn, T, H, frames, layout):
         R.close(g, want[name], tol[name], name)
 
 
+@pytest.mark.parametrize("Bn", [33, 64, 70])
+def test_attention_many_ragged_clips(Bn):
+    """Up to 64 clips are ordered by length, more are taken as they come; some are empty, some equal."""
+    gen = torch.Generator().manual_seed(Bn)
+    frames = torch.randint(0, 300, (Bn,), generator=gen).tolist()
+    frames[3] = frames[7] = 0
+    frames[5] = frames[6]
+    frames[1] = 300
+    case = _attention_case(BF16, Bn, 300, 2, frames, "fused")
+    t3, do, q, k, v, fr = case
+    out, lse, grads = _run_attention(*case, "fused")
+    want, tol, lse64 = R.attention(t3[:, :, 0], t3[:, :, 1], t3[:, :, 2], 2, frames, do, out.cpu())
+    R.close(out, want["out"], tol["out"], "out")
+    assert torch.equal(lse.cpu() == -math.inf, lse64 == -math.inf)
+    for name, g in zip(("dq", "dk", "dv"), grads):
+        R.close(g, want[name], tol[name], name)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_of_nothing_but_padding(dtype):
+    case = _attention_case(dtype, 3, 140, 2, [0, 0, 0], "dense")
+    out, lse, grads = _run_attention(*case, "dense")
+    assert (out == 0).all() and (lse == -math.inf).all() and all((g == 0).all() for g in grads)
+
+
+def test_attention_strides_of_single_entries_do_not_matter():
+    """A clip of one frame, and a batch of one: torch may give these axes any stride."""
+    gen = torch.Generator().manual_seed(8)
+    q, k, v = (_rand(gen, 4, 1, 128).half().cuda() for _ in range(3))
+    odd = torch.empty(4, 130, dtype=F16, device="cuda")  # row stride 130, unusable if it were used
+    out, lse, err = torch.empty_like(q), torch.empty(4, 2, 1, device="cuda"), _err()
+    kk = torch.as_strided(k, (4, 1, 128), (128, 77, 1))
+    B.w2v_op_attention_fwd(q, kk, v, out, lse, err)
+    assert torch.equal(out, v)  # one key: the output is its value
+    one = torch.as_strided(q, (1, 4, 128), (13, 128, 1))
+    res, l2 = torch.empty(1, 4, 128, dtype=F16, device="cuda"), torch.empty(1, 2, 4, device="cuda")
+    B.w2v_op_attention_fwd(one, one, one, res, l2, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.isfinite(res).all() and odd.shape == (4, 130)
+
+
+def test_attention_bindings_refuse_what_the_kernels_cannot_see():
+    q = torch.zeros(2, 8, 128, dtype=F16, device="cuda")
+    lse, err = torch.zeros(2, 2, 8, device="cuda"), _err()
+    bad = [dict(k=q.float()), dict(v=q[:, :7]), dict(k=q.transpose(0, 1).contiguous().transpose(0, 1)),
+           dict(lse=lse.double()), dict(lse=lse[:, :, :7]), dict(err=err.float()), dict(k=q.cpu()),
+           dict(frames=torch.zeros(2, device="cuda")), dict(frames=torch.zeros(3, dtype=torch.int32, device="cuda")),
+           dict(q=torch.zeros(2, 8, 100, dtype=F16, device="cuda")),
+           dict(v=torch.zeros(2, 8, 256, dtype=F16, device="cuda")[:, :, ::2])]
+    for change in bad:
+        a = dict(q=q, k=q, v=q, out=q, lse=lse, err=err)
+        a.update(change)
+        with pytest.raises(B.W2VError):
+            B.w2v_op_attention_fwd(**a)
+    with pytest.raises(B.W2VError):  # expanded over the batch: no stride to walk
+        e = q[:1].expand(2, 8, 128)
+        B.w2v_op_attention_fwd(e, e, e, q, lse, err)
+    with pytest.raises(B.W2VError):
+        B.w2v_op_attention_bwd(q, q, q, q, q, lse, q, q, q, err, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+def test_attention_calls_at_once_on_two_streams():
+    cases = [_attention_case(F16, 2, 500, 4, [500, 210], "fused"), _attention_case(BF16, 3, 333, 4, [1, 333, 90], "dense")]
+    alone = [_run_attention(*c, lay) for c, lay in zip(cases, ("fused", "dense"))]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    runs = []
+    for (t3, do, q, k, v, fr), s in zip(cases, streams):
+        with torch.cuda.stream(s):
+            err, dout = _err(), do.cuda()
+            out, lse = torch.empty_like(q.contiguous()), torch.empty(q.shape[0], 4, q.shape[1], device="cuda")
+            grads = [torch.empty_like(out) for _ in range(3)]
+            for _ in range(5):
+                B.w2v_op_attention_fwd(q, k, v, out, lse, err, frames=fr)
+                B.w2v_op_attention_bwd(dout, q, k, v, out, lse, *grads, err, frames=fr)
+            runs.append((out, grads, err))
+    torch.cuda.synchronize()
+    for (out, grads, err), one in zip(runs, alone):
+        assert int(err.item()) == 0
+        assert torch.equal(out, one[0]) and all(torch.equal(x, y) for x, y in zip(grads, one[2]))
+
+
 def test_attention_leaves_what_lies_between_rows():
     """Rows longer than the heads' width: the columns and rows in between keep their contents."""
     dtype, Bn, T, H = F16, 2, 70, 2
@@ -143,17 +225,14 @@ def test_attention_repeats_bit_for_bit_whatever_the_workspace_holds():
     assert torch.equal(first[0], again[0]) and all(torch.equal(x, y) for x, y in zip(first[2], again[2]))
 
 
-@pytest.mark.parametrize("exponent", [-14, -6, 6])
+@pytest.mark.parametrize("exponent", [-18, -14, -6, 6, 12])
 def test_attention_fp16_gradients_scale_with_dout(exponent):
-    """dS is held in fp16 under a scale of its own: gradients of small and large dout are as exact as any.
-    The last factor makes the smallest dq a normal fp16 number."""
+    """dS is held in fp16 under a scale of its own, the row sums in pieces of their own: gradients of small and
+    large dout are as exact as any (half a step of what fp16 can still say of them)."""
     case = list(_attention_case(F16, 1, 160, 2, None, "dense"))
-    t3, q = case[0], case[2]
-    # dout a power of two apart: outputs must be exactly that power apart while they stay normal
+    t3 = case[0]
     base = _run_attention(*case, "dense")
     case[1] = (case[1].float() * 2.0 ** exponent).half()
-    if not torch.equal(case[1].float(), case[1].float()):
-        pytest.skip("not representable")
     moved = _run_attention(*case, "dense")
     want, tol, _ = R.attention(t3[:, :, 0], t3[:, :, 1], t3[:, :, 2], 2, None, case[1], moved[0].cpu())
     for name, g in zip(("dq", "dk", "dv"), moved[2]):
@@ -182,6 +261,23 @@ def test_attention_sharp_and_extreme_scores():
     R.close(out, want["out"], tol["out"] * (1 + extra / R.half_step(F16)), "out")
     for name, g in zip(("dq", "dk", "dv"), grads):
         R.close(g, want[name], tol[name] * (1 + extra / R.half_step(F16)), name)
+
+
+def test_attention_fp16_log_sum_exp_beyond_the_first_constant():
+    """Scores of 2^21: one key takes all the weight, exactly; 8 lse needs the second group of fp16 pieces."""
+    gen = torch.Generator().manual_seed(13)
+    T = 140
+    sign = torch.sign(_rand(gen, T, 64))
+    t3 = torch.stack([512 * sign, 512 * sign, _rand(gen, T, 64)], 1)[None].half()
+    do = _rand(gen, 1, T, 64).half()
+    q, k, v = _triple(t3, "dense")
+    out, lse, grads = _run_attention(t3, do, q, k, v, None, "dense")
+    assert torch.equal(out, v) and (lse == 2.0 ** 21).all()
+    assert torch.equal(grads[2].cpu(), do)
+    # dP and the row sum are one number summed in two orders: 64 * 2^-23 of its magnitude, times 512 / 8
+    mag = (do.double().abs() * t3[:, :, 2].double().abs()).sum(2, keepdim=True)
+    for g in grads[:2]:
+        assert (g.double().cpu().abs() <= 64 * 64 * 2.0 ** -23 * mag + R.tiny(F16)).all()
 
 
 def test_attention_gradient_against_differences():

@@ -58,6 +58,8 @@ def test_attention_pointers_refused(bad):
     assert _fwd(s, lse=None) == B.W2V_EINVAL
     assert _fwd(s, lse=P + 2) == B.W2V_EINVAL
     assert _fwd(s, err=None) == B.W2V_EINVAL
+    assert _fwd(s, err=P + 1) == B.W2V_EINVAL
+    assert _fwd(_shape(frames=P + 2)) == B.W2V_EINVAL
     assert _fwd(None) == B.W2V_EINVAL
 
 
