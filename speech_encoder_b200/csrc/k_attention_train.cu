@@ -614,6 +614,12 @@ attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __r
 // <= 2 max|dout| max|v| (out_i is a mean of v rows), so with that bound brought
 // just under 2^15 no entry overflows and the smallest keep what precision fp16
 // can give them.  Every thread of the warp gets the same value.
+__device__ __forceinline__ int ds_exponent(float top_do, float top_v) {
+  const float bound = 2.0f * sqrtf(top_do) * sqrtf(top_v);
+  if (!(bound > 0.f) || !(bound < INFINITY)) return 0;
+  return max(-100, min(100, 14 - ilogbf(bound)));
+}
+
 __device__ __forceinline__ int ds_exponent(const float2* peak, int tiles, int lane) {
   float top_do = 0.f, top_v = 0.f;
   for (int i = lane; i < tiles; i += 32) {
@@ -626,9 +632,7 @@ __device__ __forceinline__ int ds_exponent(const float2* peak, int tiles, int la
     top_do = fmaxf(top_do, __shfl_xor_sync(0xffffffffu, top_do, o));
     top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
   }
-  const float bound = 2.0f * sqrtf(top_do) * sqrtf(top_v);
-  if (!(bound > 0.f) || !(bound < INFINITY)) return 0;
-  return max(-100, min(100, 14 - ilogbf(bound)));
+  return ds_exponent(top_do, top_v);
 }
 
 // ------------------------------------------------------------------- backward
@@ -658,7 +662,7 @@ struct BwdSmem {
   static constexpr int AugB = AugA + 2 * 128 * kAugRow;      // [stages]{lse, rowsum} of the streamed rows
   static constexpr int kAugTile = kSub * kAugRow;
   static constexpr int BAR = AugB + kStages * 2 * kAugTile;
-  static constexpr int TOTAL = BAR + 256 + 1024;
+  static constexpr int TOTAL = BAR + 256 + 1024;  // barriers and the TMEM address, then (at 192) 64 bytes of reductions
 };
 constexpr int kBwdThreads = 320;
 
@@ -670,7 +674,79 @@ struct BwdArgs {
   const float2* peak;
   int T, H, batch, tiles;
   int* err;
+  // For T <= 128 a CTA makes the statistics of its clip itself (they are one tile's)
+  // and no other kernel runs before this one (49 frames x 12 heads: 5.9 us and one
+  // launch, against 8.0 and two); null otherwise.
+  const uint16_t* dout;
+  const uint16_t* out;
+  const uint16_t* v;
+  const float* lse;
+  int64_t out_ld, out_bs, v_ld, v_bs;
 };
+
+// The statistics of one clip of at most 128 frames, as attention_bwd_rows_kernel
+// makes them, straight into shared memory: two threads a row (warps 0-7).  Returns
+// the exponent of dS's scale.
+template <bool BF16, bool KEYS>
+__device__ __forceinline__ int own_statistics(const BwdArgs& a, uint8_t* smem, int b, int h, int len) {
+  float* red = reinterpret_cast<float*>(smem + BwdSmem::BAR + 192);  // [8 warps]{dout, v} of 8 bytes: see below
+  const int row = threadIdx.x >> 1, part = threadIdx.x & 1;
+  float top_do = 0.f, top_v = 0.f;
+  if (threadIdx.x < 256) {
+    float d = 0.f, l = -INFINITY;
+    if (row < len) {
+      const int64_t at = b * a.out_bs + row * a.out_ld + h * kHd + part * 32;
+      const int64_t va = b * a.v_bs + row * a.v_ld + h * kHd + part * 32;
+#pragma unroll
+      for (int c = 0; c < 32; c += 8) {
+        const uint4 x4 = *reinterpret_cast<const uint4*>(a.dout + at + c);
+        const uint4 y4 = *reinterpret_cast<const uint4*>(a.out + at + c);
+        uint4 z4 = make_uint4(0, 0, 0, 0);
+        if (!BF16) z4 = *reinterpret_cast<const uint4*>(a.v + va + c);
+        const uint32_t xu[4] = {x4.x, x4.y, x4.z, x4.w}, yu[4] = {y4.x, y4.y, y4.z, y4.w};
+        const uint32_t zu[4] = {z4.x, z4.y, z4.z, z4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = unpack2<BF16>(xu[i]), y = unpack2<BF16>(yu[i]), z = unpack2<BF16>(zu[i]);
+          d = fmaf(x.x, y.x, fmaf(x.y, y.y, d));
+          if (!BF16) {
+            top_do = fmaf(x.x, x.x, fmaf(x.y, x.y, top_do));
+            top_v = fmaf(z.x, z.x, fmaf(z.y, z.y, top_v));
+          }
+        }
+      }
+      l = a.lse[(static_cast<int64_t>(b) * a.H + h) * a.T + row];
+    }
+    d += __shfl_xor_sync(0xffffffffu, d, 1);
+    const float value = part ? -d : (l == -INFINITY ? -INFINITY : -8.0f * l);
+    uint8_t* dst = KEYS ? smem + BwdSmem::AugB + (row >> 6) * 2 * BwdSmem::kAugTile + part * BwdSmem::kAugTile
+                        : smem + BwdSmem::AugA + part * 128 * kAugRow;
+    const int at = KEYS ? row & 63 : row;
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+      *reinterpret_cast<uint4*>(dst + aug_offset(at, half)) = aug_pieces<BF16>(value, part, half);
+    if (!BF16) {
+      top_do += __shfl_xor_sync(0xffffffffu, top_do, 1);
+      top_v += __shfl_xor_sync(0xffffffffu, top_v, 1);
+#pragma unroll
+      for (int o = 2; o < 32; o <<= 1) {
+        top_do = fmaxf(top_do, __shfl_xor_sync(0xffffffffu, top_do, o));
+        top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
+      }
+      if ((threadIdx.x & 31) == 0) {
+        red[threadIdx.x >> 4] = top_do;
+        red[(threadIdx.x >> 4) + 1] = top_v;
+      }
+      named_barrier_sync(1, 256);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        top_do = fmaxf(top_do, red[2 * i]);
+        top_v = fmaxf(top_v, red[2 * i + 1]);
+      }
+    }
+  }
+  return BF16 ? 0 : ds_exponent(top_do, top_v);
+}
 
 template <bool BF16, bool KEYS>
 __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensorMap& tmA2, const CUtensorMap& tmB1,
@@ -693,8 +769,13 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
   const int b = unit.b, h = unit.h, tile = unit.tile, len = unit.len;
   const int64_t bh = static_cast<int64_t>(b) * a.H + h;
   const int n_sub = (len + kSub - 1) / kSub;
-  if (tile * 128 >= len) {  // padded rows, in a batch that is taken as it comes
+  if (tile * 128 >= len) {  // padded rows, in a batch that is taken as it comes or (own statistics) an empty clip
     if (threadIdx.x == 0) pdl_launch_dependents();
+    if (a.dout) {
+      const int64_t at = b * a.g.bs + h * kHd;
+      zero_rows((KEYS ? a.g.dk : a.g.dq) + at, a.g.ld, 0, a.T);
+      if (KEYS) zero_rows(a.g.dv + at, a.g.ld, 0, a.T);
+    }
     return;
   }
 
@@ -723,6 +804,11 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
     uint8_t* dst = KEYS ? smem + BwdSmem::AugA + rowsum * 128 * kAugRow : smem + BwdSmem::AugB + rowsum * BwdSmem::kAugTile;
     *reinterpret_cast<uint4*>(dst + aug_offset(row, half)) = aug_constants<BF16>(rowsum, half);
   }
+  int e = 0;  // of dS's scale (see below)
+  if (a.dout) {
+    if (!a.frames) pdl_wait();
+    e = own_statistics<BF16, KEYS>(a, smem, b, h, len);
+  }
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -730,18 +816,18 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
   const uint32_t tmem = uniform(*tmem_slot);
   // dV (key CTA) | dK or dQ | S | dP, then dS and P
   const uint32_t tAcc1 = tmem, tAcc2 = tmem + 64, tS = tmem + 128, tD = tmem + 192;
-  if (!a.frames) pdl_wait();
+  if (!a.frames && !a.dout) pdl_wait();
 
   if (warp == 8) {
     if (lane == 0) {
-      mbar_arrive_expect_tx(a_full, 4 * kTileBytes + (KEYS ? 0 : 2 * 128 * kAugRow));
+      mbar_arrive_expect_tx(a_full, 4 * kTileBytes + (KEYS || a.dout ? 0 : 2 * 128 * kAugRow));
       for (int i = 0; i < 2; ++i) {
         tma_load_3d(smem + BwdSmem::A + i * kTileBytes, &tmA1, a_full, h * kHd, tile * 128 + i * kSub, b);
         tma_load_3d(smem + BwdSmem::A + (2 + i) * kTileBytes, &tmA2, a_full, h * kHd, tile * 128 + i * kSub, b);
       }
       const uint8_t* al = a.aug_l + bh * a.tiles * 128 * kAugRow;
       const uint8_t* ad = a.aug_d + bh * a.tiles * 128 * kAugRow;
-      if (!KEYS) {
+      if (!KEYS && !a.dout) {
         bulk_load(smem + BwdSmem::AugA, al + tile * 128 * kAugRow, 128 * kAugRow, a_full);
         bulk_load(smem + BwdSmem::AugA + 128 * kAugRow, ad + tile * 128 * kAugRow, 128 * kAugRow, a_full);
       }
@@ -755,10 +841,10 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
           break;
         }
         uint8_t* dst = smem + BwdSmem::B + st * 2 * kTileBytes;
-        mbar_arrive_expect_tx(&b_full[st], 2 * kTileBytes + (KEYS ? 2 * BwdSmem::kAugTile : 0));
+        mbar_arrive_expect_tx(&b_full[st], 2 * kTileBytes + (KEYS && !a.dout ? 2 * BwdSmem::kAugTile : 0));
         tma_load_3d(dst, &tmB1, &b_full[st], h * kHd, j * kSub, b);
         tma_load_3d(dst + kTileBytes, &tmB2, &b_full[st], h * kHd, j * kSub, b);
-        if (KEYS) {
+        if (KEYS && !a.dout) {
           uint8_t* aug = smem + BwdSmem::AugB + st * 2 * BwdSmem::kAugTile;
           bulk_load(aug, al + j * BwdSmem::kAugTile, BwdSmem::kAugTile, &b_full[st]);
           bulk_load(aug + BwdSmem::kAugTile, ad + j * BwdSmem::kAugTile, BwdSmem::kAugTile, &b_full[st]);
@@ -861,7 +947,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
     // fp16: dS is scaled by 2^(up + down).  Up to 2^15 of it goes into P (which is
     // at most 1, and is as exact scaled as unscaled), and so into dV too; what
     // shrinks dS is a factor of its own.
-    const int e = BF16 ? 0 : ds_exponent(a.peak + bh * a.tiles, a.tiles, lane);
+    if (!BF16 && !a.dout) e = ds_exponent(a.peak + bh * a.tiles, a.tiles, lane);
     const int up = max(0, min(15, e)), down = min(0, e);
     const float shift = static_cast<float>(up), shrink = exp2f(static_cast<float>(down));
     bool ok = true;
@@ -962,12 +1048,14 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     pdl_wait();
     live = live_units(a.frames, a.batch, a.T, a.H, live, threadIdx.x & 31);
   }
-  const int u = blockIdx.x;
-  if (u >= 2 * live) return;
-  if (u < live)
-    bwd_body<BF16, true>(tmK, tmV, tmQ, tmDo, a, u);
+  // (with its own statistics the kernel also writes the zeros of empty clips: there
+  // the units without frames follow, key units first)
+  const int u = blockIdx.x, units = a.tiles * a.batch * a.H;
+  if (u >= 2 * live && !a.dout) return;
+  if (u < live || (u >= 2 * live && u < units + live))
+    bwd_body<BF16, true>(tmK, tmV, tmQ, tmDo, a, u < live ? u : u - live);
   else
-    bwd_body<BF16, false>(tmQ, tmDo, tmK, tmV, a, u - live);
+    bwd_body<BF16, false>(tmQ, tmDo, tmK, tmV, a, u < 2 * live ? u - live : u - units);
 }
 
 // [batch][T][H][64] operand as {H * 64, T, batch}, 64-row boxes of one head.
@@ -1018,10 +1106,19 @@ cudaError_t launch_attention_bwd(const AttnTrain& s, const void* dout, const voi
   auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
   BwdArgs a;
   a.g = {static_cast<uint16_t*>(dq), static_cast<uint16_t*>(dk), static_cast<uint16_t*>(dv), s.grad_ld, s.grad_bs};
-  r = launch_pdl(s.bf16 ? attention_bwd_rows_kernel<true> : attention_bwd_rows_kernel<false>, dim3(tiles * bh),
-                 dim3(256), 0, st, u16(dout), u16(out), s.out_ld, s.out_bs, u16(v), s.qkv_ld, s.qkv_bs, lse, s.frames,
-                 s.T, s.H, tiles, aug_l, aug_d, peak, a.g);
-  if (r != cudaSuccess) return r;
+  const bool own = tiles == 1;
+  if (!own) {
+    r = launch_pdl(s.bf16 ? attention_bwd_rows_kernel<true> : attention_bwd_rows_kernel<false>, dim3(tiles * bh),
+                   dim3(256), 0, st, u16(dout), u16(out), s.out_ld, s.out_bs, u16(v), s.qkv_ld, s.qkv_bs, lse,
+                   s.frames, s.T, s.H, tiles, aug_l, aug_d, peak, a.g);
+    if (r != cudaSuccess) return r;
+  }
+  a.dout = own ? u16(dout) : nullptr;
+  a.out = u16(out);
+  a.v = u16(v);
+  a.lse = lse;
+  a.out_ld = s.out_ld; a.out_bs = s.out_bs;
+  a.v_ld = s.qkv_ld; a.v_bs = s.qkv_bs;
   a.frames = s.frames;
   a.aug_l = aug_l;
   a.aug_d = aug_d;
