@@ -9,7 +9,7 @@
  * to the next, so each may be recorded into a CUDA graph.  Scratch is a
  * workspace that the caller passes (16-byte aligned device memory of at least
  * the size its w2v_op_*_workspace function returns; nothing in it needs to be
- * initialised or kept).  Calls whose work may overlap on the GPU — two
+ * initialised or kept; a size of 0 means that NULL will do).  Calls whose work may overlap on the GPU — two
  * streams, two graphs — need a workspace each.
  *
  * Sums run in a fixed order: the same call gives the same bits.
@@ -56,7 +56,8 @@ typedef struct {
 int w2v_op_attention_fwd(const w2v_attention_shape* shape, const void* q, const void* k, const void* v, void* out,
                          float* lse, int* err_dev, void* stream);
 
-/* Bytes of the backward pass's workspace (0 if batch, T or H < 1). */
+/* Bytes of the backward pass's workspace (0 up to 128 frames, and if batch, T or
+ * H < 1). */
 size_t w2v_op_attention_bwd_workspace(int batch, int T, int H);
 
 /* Gradients of w2v_op_attention_fwd: with P = exp(q k^T / 8 - lse),
@@ -90,7 +91,8 @@ int w2v_op_layernorm_fwd(const void* x, int x_type, int64_t x_ld, void* y, int y
                          int cols, const float* gamma, const float* beta, float eps, int act, float* mean, float* rstd,
                          void* stream);
 
-/* Bytes of the backward pass's workspace (0 if a size is out of range). */
+/* Bytes of the backward pass's workspace (0 for few rows, and if a size is out of
+ * range). */
 size_t w2v_op_layernorm_bwd_workspace(int64_t rows, int cols);
 
 /* Gradients of w2v_op_layernorm_fwd (and of w2v_op_layernorm, with the mean and

@@ -1086,6 +1086,7 @@ cudaError_t launch_attention_fwd(const AttnTrain& s, const void* q, const void* 
 
 size_t attention_bwd_ws_bytes(int batch, int T, int H) {
   const size_t tiles = (static_cast<size_t>(T) + 127) / 128, bh = static_cast<size_t>(batch) * H;
+  if (tiles == 1) return 0;  // the statistics stay in shared memory
   return bh * tiles * (128 * 2 * kAugRow + sizeof(float2));
 }
 

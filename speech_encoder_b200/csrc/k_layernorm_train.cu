@@ -658,6 +658,7 @@ cudaError_t launch_layernorm_fwd(const LnTrain& s, const void* x, void* y, float
 }
 
 size_t layernorm_bwd_ws_bytes(int64_t rows, int cols) {
+  if (bwd_in_cluster(rows, cols)) return 0;
   return static_cast<size_t>(bwd_blocks(rows, cols)) * 2 * cols * sizeof(float);
 }
 

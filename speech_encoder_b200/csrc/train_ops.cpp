@@ -79,6 +79,11 @@ size_t type_size(int t) { return t == W2V_F32 ? 4 : 2; }
 
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// A workspace of no bytes may be anything.
+bool workspace_ok(const void* ws, size_t has, size_t needs) {
+  return needs == 0 || (ws && aligned16(ws) && has >= needs);
+}
+
 }  // namespace
 
 extern "C" int w2v_op_attention_fwd(const w2v_attention_shape* shape, const void* q, const void* k, const void* v,
@@ -104,12 +109,12 @@ extern "C" int w2v_op_attention_bwd(const w2v_attention_shape* shape, const void
   AttnTrain a;
   const int rc = attention_args(shape, true, &a);
   if (rc != W2V_OK) return rc;
-  if (!dout || !q || !k || !v || !out || !lse || !dq || !dk || !dv || !ws || !err_dev) return W2V_EINVAL;
+  if (!dout || !q || !k || !v || !out || !lse || !dq || !dk || !dv || !err_dev) return W2V_EINVAL;
   for (const void* p : {dout, q, k, v, out, static_cast<const void*>(dq), static_cast<const void*>(dk),
-                        static_cast<const void*>(dv), static_cast<const void*>(ws)})
+                        static_cast<const void*>(dv)})
     if (!aligned16(p)) return W2V_EINVAL;
   if (!aligned_to(lse, 4) || !aligned_to(err_dev, 4)) return W2V_EINVAL;
-  if (ws_bytes < attention_bwd_ws_bytes(a.batch, a.T, a.H)) return W2V_EINVAL;
+  if (!workspace_ok(ws, ws_bytes, attention_bwd_ws_bytes(a.batch, a.T, a.H))) return W2V_EINVAL;
   return status(launch_attention_bwd(a, dout, q, k, v, out, lse, dq, dk, dv, ws, err_dev,
                                      static_cast<cudaStream_t>(stream)));
 }
@@ -141,13 +146,13 @@ extern "C" int w2v_op_layernorm_bwd(const void* dy, int y_type, int64_t dy_ld, c
   LnTrain a;
   const int rc = layernorm_args(x_type, x_ld, y_type, dy_ld, rows, cols, gamma, beta, act, &a);
   if (rc != W2V_OK) return rc;
-  if (!dgamma || !dbeta || !ws || (rows > 0 && (!dy || !x || !mean || !rstd || !dx))) return W2V_EINVAL;
+  if (!dgamma || !dbeta || (rows > 0 && (!dy || !x || !mean || !rstd || !dx))) return W2V_EINVAL;
   if (dx_ld < cols || (dres && dres_ld < cols) || (dres && dres == dx && dres_ld != dx_ld)) return W2V_EINVAL;
   if (!aligned_to(dy, type_size(y_type)) || !aligned_to(x, type_size(x_type)) || !aligned_to(dx, type_size(x_type)) ||
       !aligned_to(dres, type_size(x_type)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(gamma, 4) ||
-      !aligned_to(beta, 4) || !aligned_to(dgamma, 4) || !aligned_to(dbeta, 4) || !aligned16(ws))
+      !aligned_to(beta, 4) || !aligned_to(dgamma, 4) || !aligned_to(dbeta, 4))
     return W2V_EINVAL;
-  if (ws_bytes < layernorm_bwd_ws_bytes(rows, cols)) return W2V_EINVAL;
+  if (!workspace_ok(ws, ws_bytes, layernorm_bwd_ws_bytes(rows, cols))) return W2V_EINVAL;
   return status(launch_layernorm_bwd(a, dy, x, mean, rstd, dres, dres_ld, dx, dx_ld, dgamma, dbeta, ws,
                                      static_cast<cudaStream_t>(stream)));
 }
@@ -158,10 +163,10 @@ extern "C" int w2v_op_grad_clip(int n, const void* const* grads, void* const* ou
                                 const int* types, float scale, float max_norm, float* norm_dev, void* ws,
                                 size_t ws_bytes, void* stream) {
   if (n < 0) return W2V_ESHAPE;
-  if (!norm_dev || !ws || !aligned_to(norm_dev, 4) || !aligned16(ws)) return W2V_EINVAL;
+  if (!norm_dev || !aligned_to(norm_dev, 4)) return W2V_EINVAL;
   if (n > 0 && (!grads || !outs || !counts || !types)) return W2V_EINVAL;
   if (!(scale > 0.f) || !(scale < INFINITY) || !(max_norm > 0.f)) return W2V_EINVAL;
-  if (ws_bytes < grad_clip_ws_bytes(n)) return W2V_EINVAL;
+  if (!workspace_ok(ws, ws_bytes, grad_clip_ws_bytes(n))) return W2V_EINVAL;
   try {
     // Byte ranges written, and each tensor's read range: an output may be its own
     // gradient's memory, and nothing else that the call reads or writes.

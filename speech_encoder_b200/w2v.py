@@ -396,16 +396,21 @@ def _torch():
 
 
 def _workspace(ws, nbytes: int, device, stream):
-    """The caller's workspace, or one from torch's allocator, owned by the stream that the call runs on."""
-    torch = _torch()
+    """(pointer, bytes, owner) of the caller's workspace, or of one from torch's allocator, owned by the stream
+    that the call runs on."""
     if ws is not None:
         if not ws.is_contiguous() or ws.device != device:
             _refuse("workspace: not contiguous, or on another device")
-        return ws, ws.numel() * ws.element_size()
+        return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+    if nbytes == 0:
+        return None, 0, None
+    torch = _torch()
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
-    with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=device)):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=device)):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws.data_ptr(), nbytes, ws
 
 
 def _row_strides(what: str, shape, tensors):
@@ -463,9 +468,9 @@ def w2v_op_attention_bwd(dout, q, k, v, out, lse, dq, dk, dv, err, frames=None, 
     have equal strides, as have dq, dk and dv.  ws: a workspace of
     w2v_op_attention_bwd_workspace bytes, or None for one from torch's allocator."""
     s = _attention_shape((q, k, v), (out, dout), (dq, dk, dv), lse, err, frames)
-    ws, nbytes = _workspace(ws, w2v_op_attention_bwd_workspace(s.batch, s.T, s.H), q.device, stream)
+    ws, nbytes, _owner = _workspace(ws, w2v_op_attention_bwd_workspace(s.batch, s.T, s.H), q.device, stream)
     _check(lib().w2v_op_attention_bwd(s, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                      lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
+                                      lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws,
                                       nbytes, err.data_ptr(), _stream(stream)), None, "w2v_op_attention_bwd")
 
 
@@ -520,13 +525,13 @@ def w2v_op_layernorm_bwd(dy, x, gamma, beta, mean, rstd, act: int, dres, dx, dga
     _norm_vectors(rows, (mean, rstd))
     if dx.dtype != x.dtype or (dres is not None and dres.dtype != x.dtype):
         _refuse("layernorm: dx or dres is not of x's type")
-    ws, nbytes = _workspace(ws, w2v_op_layernorm_bwd_workspace(rows, cols), x.device, stream)
+    ws, nbytes, _owner = _workspace(ws, w2v_op_layernorm_bwd_workspace(rows, cols), x.device, stream)
     _check(lib().w2v_op_layernorm_bwd(dy.data_ptr(), _type_code(dy.dtype), _norm_rows("dy", dy, shape), x.data_ptr(),
                                       _type_code(x.dtype), _norm_rows("x", x, shape), rows, cols, gamma.data_ptr(),
                                       beta.data_ptr(), mean.data_ptr(), rstd.data_ptr(), act,
                                       None if dres is None else dres.data_ptr(),
                                       0 if dres is None else _norm_rows("dres", dres, shape), dx.data_ptr(),
-                                      _norm_rows("dx", dx, shape), dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(),
+                                      _norm_rows("dx", dx, shape), dgamma.data_ptr(), dbeta.data_ptr(), ws,
                                       nbytes, _stream(stream)), None, "w2v_op_layernorm_bwd")
 
 
@@ -556,9 +561,9 @@ def w2v_op_grad_clip(grads, outs, scale: float, max_norm: float, norm, ws=None, 
     code = {t: _type_code(t) for t in set(types)}
     types = array.array("i", [code[t] for t in types])
     src, dst = array.array("Q", map(Tensor.data_ptr, grads)), array.array("Q", map(Tensor.data_ptr, outs))
-    ws, nbytes = _workspace(ws, w2v_op_grad_clip_workspace(n), norm.device, stream)
+    ws, nbytes, _owner = _workspace(ws, w2v_op_grad_clip_workspace(n), norm.device, stream)
     _check(lib().w2v_op_grad_clip(n, src.buffer_info()[0], dst.buffer_info()[0], counts.buffer_info()[0],
-                                  types.buffer_info()[0], scale, max_norm, norm.data_ptr(), ws.data_ptr(), nbytes,
+                                  types.buffer_info()[0], scale, max_norm, norm.data_ptr(), ws, nbytes,
                                   _stream(stream)), None, "w2v_op_grad_clip")
 
 

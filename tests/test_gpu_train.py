@@ -163,7 +163,9 @@ def test_attention_bindings_refuse_what_the_kernels_cannot_see():
         e = q[:1].expand(2, 8, 128)
         B.w2v_op_attention_fwd(e, e, e, q, lse, err)
     with pytest.raises(B.W2VError):
-        B.w2v_op_attention_bwd(q, q, q, q, q, lse, q, q, q, err, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        w = torch.zeros(1, 300, 128, dtype=F16, device="cuda")
+        B.w2v_op_attention_bwd(w, w, w, w, w, torch.zeros(1, 2, 300, device="cuda"), w, w, w, err,
+                               ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
 
 
 def test_attention_calls_at_once_on_two_streams():

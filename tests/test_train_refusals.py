@@ -53,7 +53,7 @@ def test_attention_pointers_refused(bad):
     s = _shape()
     for name in ("q", "k", "v", "out"):
         assert _fwd(s, **{name: bad}) == B.W2V_EINVAL, name
-    for name in ("dout", "q", "k", "v", "out", "dq", "dk", "dv", "ws"):
+    for name in ("dout", "q", "k", "v", "out", "dq", "dk", "dv"):
         assert _bwd(s, **{name: bad}) == B.W2V_EINVAL, name
     assert _fwd(s, lse=None) == B.W2V_EINVAL
     assert _fwd(s, lse=P + 2) == B.W2V_EINVAL
@@ -64,9 +64,13 @@ def test_attention_pointers_refused(bad):
 
 
 def test_attention_workspace():
-    n = B.w2v_op_attention_bwd_workspace(2, 10, 4)
+    n = B.w2v_op_attention_bwd_workspace(2, 200, 4)
     assert n > 0
-    assert _bwd(_shape(), ws_bytes=n - 1) == B.W2V_EINVAL
+    s = _shape(T=200, qkv_bs=51200, out_bs=51200, grad_bs=51200)
+    assert _bwd(s, ws_bytes=n - 1) == B.W2V_EINVAL
+    for ws in (None, P + 8):
+        assert _bwd(s, ws=ws) == B.W2V_EINVAL
+    assert B.w2v_op_attention_bwd_workspace(2, 128, 4) == 0
     assert B.w2v_op_attention_bwd_workspace(0, 10, 4) == 0
     assert B.w2v_op_attention_bwd_workspace(2, 0, 4) == 0
     # sizes past 32 bits are counted in 64
@@ -104,10 +108,11 @@ def test_layernorm_one_sided_refusals():
     assert _ln_fwd(eps=math.nan) == B.W2V_EINVAL
     assert _ln_fwd(y_ld=10) == B.W2V_EINVAL
     for change in (dict(dx_ld=10), dict(dy_ld=10), dict(dres=P, dres_ld=10), dict(dx=None), dict(dgamma=None),
-                   dict(dbeta=P + 1), dict(ws=None), dict(ws=P + 4), dict(dres=P, dres_ld=128)):
+                   dict(dbeta=P + 1), dict(rows=5000, ws=None), dict(rows=5000, ws=P + 4), dict(dres=P, dres_ld=128)):
         assert _ln_bwd(**change) == B.W2V_EINVAL, change
-    n = B.w2v_op_layernorm_bwd_workspace(3, 64)
-    assert n > 0 and _ln_bwd(ws_bytes=n - 1) == B.W2V_EINVAL
+    n = B.w2v_op_layernorm_bwd_workspace(5000, 64)
+    assert n > 0 and _ln_bwd(rows=5000, ws_bytes=n - 1) == B.W2V_EINVAL
+    assert B.w2v_op_layernorm_bwd_workspace(3, 64) == 0
     assert B.w2v_op_layernorm_bwd_workspace(-1, 64) == 0
     assert B.w2v_op_layernorm_bwd_workspace(3, 8193) == 0
 
