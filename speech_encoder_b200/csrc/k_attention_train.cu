@@ -194,7 +194,7 @@ __device__ __forceinline__ void stage_row_part(uint32_t taddr, uint8_t* tile, in
 
 // A staged tile to rows [0, rows) of one head, eight threads a row (a thread per
 // row, straight from its registers, writes 32 lines an instruction and took 2.3 us
-// for two tiles where this takes 0.9).
+// for two tiles where this takes 1.5).
 __device__ __forceinline__ void store_tile(const uint8_t* tile, uint16_t* dst, int64_t ld, int rows, int tid,
                                            int threads) {
   for (int i = tid; i < rows * 8; i += threads)
@@ -225,8 +225,8 @@ template <bool BF16>
 __global__ void __launch_bounds__(kFwdThreads, 2)
 attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const int32_t* __restrict__ frames, int T, int H,
-                     int batch, int tiles, uint16_t* __restrict__ out, int64_t out_ld, int64_t out_bs, float* __restrict__ lse,
-                     int* err) {
+                     int batch, int tiles, uint16_t* __restrict__ out, int64_t out_ld, int64_t out_bs,
+                     float* __restrict__ lse, int* err) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + FwdSmem::BAR);
@@ -418,6 +418,10 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[j % 3]);
     }
+    // The last two products in order: these scores say only that P V of tile
+    // nkv - 4 is done, and a warp may be two tiles ahead of another, so the parity of
+    // the last product's barrier alone could still be that of tile nkv - 5.
+    if (ok && nkv > 1) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[nkv & 1], ((nkv - 2) >> 1) & 1));
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(nkv - 1) & 1], ((nkv - 1) >> 1) & 1));
     const int t = qt * 128 + r;
     if (ok) {
@@ -689,7 +693,7 @@ struct BwdArgs {
 // the exponent of dS's scale.
 template <bool BF16, bool KEYS>
 __device__ __forceinline__ int own_statistics(const BwdArgs& a, uint8_t* smem, int b, int h, int len) {
-  float* red = reinterpret_cast<float*>(smem + BwdSmem::BAR + 192);  // [8 warps]{dout, v} of 8 bytes: see below
+  float* red = reinterpret_cast<float*>(smem + BwdSmem::BAR + 192);  // [8 warps]{dout, v}
   const int row = threadIdx.x >> 1, part = threadIdx.x & 1;
   float top_do = 0.f, top_v = 0.f;
   if (threadIdx.x < 256) {
