@@ -423,6 +423,25 @@ def test_layernorm_strides_and_alignment(xt, yt, offset, pad):
     _check_ln(11, 256, xt, yt, 0, offset, pad)
 
 
+@pytest.mark.parametrize("shift", [1, 2, 4])
+def test_layernorm_affine_vectors_anywhere(shift):
+    """gamma and beta inside a larger buffer, on 4-, 8- and 16-byte boundaries."""
+    x, dy, dres, gamma, beta = _ln_case(100, 512, F16, F16)
+    flat = torch.zeros(2, 512 + shift, device="cuda")
+    g, b = flat[0, shift:], torch.empty(512 + shift, device="cuda")[shift:]
+    g.copy_(gamma)
+    b.copy_(beta)
+    runs = []
+    for gg, bb in ((gamma, beta), (g, b)):
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        mean, rstd, dg, db = (torch.empty(n, device="cuda") for n in (100, 100, 512, 512))
+        B.w2v_op_layernorm_fwd(x, y, gg, bb, 1e-5, 1, mean, rstd)
+        B.w2v_op_layernorm_bwd(dy, x, gg, bb, mean, rstd, 1, dres, dx, dg, db)
+        runs.append((y, dx, dg, db))
+    for a, c in zip(*runs):  # sums of the unaligned path run in another order: a few roundings of fp32
+        assert (a.float() - c.float()).abs().max() <= 2.0 ** -10 * c.float().abs().max()
+
+
 def test_layernorm_many_rows_and_repeat():
     _check_ln(20011, 256, BF16, BF16, 1)
     x, dy, dres, gamma, beta = _ln_case(3001, 512, F16, F16)
