@@ -550,19 +550,27 @@ def w2v_op_grad_clip(grads, outs, scale: float, max_norm: float, norm, ws=None, 
     _on_current_device("grad_clip", (norm,))
     if norm.dtype != torch.float32 or norm.numel() < 1:
         _refuse("grad_clip: norm is not float32")
-    types, counts = [t.dtype for t in grads], array.array("q", map(Tensor.numel, grads))
-    devices = set(map(Tensor.get_device, grads))
-    devices.update(map(Tensor.get_device, outs))
-    if devices - {norm.get_device()}:
+    # (one pass over all tensors for each thing asked of them: on lists of small tensors these passes are the cost)
+    both = [*grads, *outs]
+    if set(map(Tensor.get_device, both)) - {norm.get_device()}:
         _refuse("grad_clip: a tensor is not on the current device")
-    if types != [t.dtype for t in outs] or counts != array.array("q", map(Tensor.numel, outs)) or not (
-            all(map(Tensor.is_contiguous, grads)) and all(map(Tensor.is_contiguous, outs))):
-        _refuse("grad_clip: outputs are not contiguous, or not like their gradients")
-    code = {t: _type_code(t) for t in set(types)}
-    types = array.array("i", [code[t] for t in types])
-    src, dst = array.array("Q", map(Tensor.data_ptr, grads)), array.array("Q", map(Tensor.data_ptr, outs))
+    if not all(map(Tensor.is_contiguous, both)):
+        _refuse("grad_clip: a tensor is not contiguous")
+    sizes = list(map(Tensor.numel, both))
+    dtypes = {t.dtype for t in both}
+    if len(dtypes) == 1:
+        types = array.array("i", [_type_code(dtypes.pop())]) * n
+    else:
+        codes = [_type_code(t.dtype) for t in both]
+        if codes[:n] != codes[n:]:
+            _refuse("grad_clip: an output is not of its gradient's type")
+        types = array.array("i", codes[:n])
+    if sizes[:n] != sizes[n:]:
+        _refuse("grad_clip: an output is not of its gradient's size")
+    counts, pointers = array.array("q", sizes[:n]), array.array("Q", list(map(Tensor.data_ptr, both)))
+    src = pointers.buffer_info()[0]
     ws, nbytes, _owner = _workspace(ws, w2v_op_grad_clip_workspace(n), norm.device, stream)
-    _check(lib().w2v_op_grad_clip(n, src.buffer_info()[0], dst.buffer_info()[0], counts.buffer_info()[0],
+    _check(lib().w2v_op_grad_clip(n, src, src + 8 * n if n else src, counts.buffer_info()[0],
                                   types.buffer_info()[0], scale, max_norm, norm.data_ptr(), ws, nbytes,
                                   _stream(stream)), None, "w2v_op_grad_clip")
 

@@ -549,6 +549,16 @@ def test_grad_clip_ranges_and_non_finite():
         assert (out[:50] == 0.5).all() and (out[51:] == 0.5).all()
 
 
+def test_grad_clip_binding_refuses_unlike_lists():
+    a, b = torch.ones(8, device="cuda"), torch.ones(8, device="cuda")
+    norm = torch.empty(1, device="cuda")
+    bad = [([a], [b, b]), ([a], [b.half()]), ([a], [b[:7]]), ([torch.ones(4, 4, device="cuda").t()], [torch.ones(4, 4, device="cuda")]),
+           ([a, b.half()], [torch.ones(8, device="cuda").half(), torch.ones(8, device="cuda")]), ([a], [b.cpu()]), ([a, a], [a, b])]
+    for grads, outs in bad:
+        with pytest.raises(B.W2VError):
+            B.w2v_op_grad_clip(grads, outs, 1.0, 1.0, norm)
+
+
 def test_grad_clip_in_a_captured_graph():
     g = torch.ones(20000, device="cuda")
     out, norm = torch.empty_like(g), torch.empty(1, device="cuda")
