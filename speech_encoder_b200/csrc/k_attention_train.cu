@@ -239,20 +239,31 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 9 + 2 * FwdSmem::kStages);
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (frames) pdl_wait();
+  // Before tensor memory is asked for: a CTA that held columns while it waited for
+  // the kernel before could keep them from a CTA of that kernel.  For the same
+  // reason the next kernel may start only once this one's columns are taken.
+  pdl_wait();
   const Unit unit = find_unit(frames, batch, T, H, tiles, blockIdx.x, lane);
   const int b = unit.b, h = unit.h, qt = unit.tile, len = unit.len;
   const int64_t bh = static_cast<int64_t>(b) * H + h;
   const int nkv = (len + kSub - 1) / kSub;
   if (qt * 128 >= len) {  // rows past the clip
-    if (threadIdx.x == 0) pdl_launch_dependents();
     const int to = min(T, qt * 128 + 128);
     zero_rows(out + b * out_bs + h * kHd, out_ld, qt * 128, to);
     for (int t = qt * 128 + threadIdx.x; t < to; t += kFwdThreads) lse[bh * T + t] = -INFINITY;
     return;
   }
 
-  if (threadIdx.x == 0) {
+  auto load_tile = [&](int j) {
+    const int st = j % FwdSmem::kStages;
+    uint8_t* dst = smem + FwdSmem::KV + st * 2 * kTileBytes;
+    mbar_arrive_expect_tx(&kv_full[st], 2 * kTileBytes);
+    tma_load_3d(dst, &tmK, &kv_full[st], h * kHd, j * kSub, b);
+    tma_load_3d(dst + kTileBytes, &tmV, &kv_full[st], h * kHd, j * kSub, b);
+  };
+  // The copying thread sets up the barriers and starts the first copies before the
+  // others have the tensor memory.
+  if (threadIdx.x == 4 * 32) {
     mbar_init(q_full, 1);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&s_full[i], 1);
@@ -265,7 +276,11 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       mbar_init(&kv_empty[i], 1);
     }
     fence_mbar_init();
-    pdl_launch_dependents();
+    fence_proxy_async_smem();
+    mbar_arrive_expect_tx(q_full, 2 * kTileBytes);
+    tma_load_3d(smem + FwdSmem::Q, &tmQ, q_full, h * kHd, qt * 128, b);
+    tma_load_3d(smem + FwdSmem::Q + kTileBytes, &tmQ, q_full, h * kHd, qt * 128 + kSub, b);
+    for (int j = 0; j < min(nkv, FwdSmem::kStages); ++j) load_tile(j);
   }
   if (warp == 5) {
     tmem_alloc(tmem_slot, 256);
@@ -276,32 +291,20 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
   const uint32_t tS = tmem, tO = tmem + 192;  // scores at 0, 64, 128
-  if (!frames) pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
 
   if (warp == 4) {
     if (lane == 0) {
-      mbar_arrive_expect_tx(q_full, 2 * kTileBytes);
-      tma_load_3d(smem + FwdSmem::Q, &tmQ, q_full, h * kHd, qt * 128, b);
-      tma_load_3d(smem + FwdSmem::Q + kTileBytes, &tmQ, q_full, h * kHd, qt * 128 + kSub, b);
-      int issued = 0;
-      bool ok = true;
-      for (int j = 0; j < nkv; ++j) {
-        const int st = j % FwdSmem::kStages;
-        if (j >= FwdSmem::kStages && !mbar_wait(&kv_empty[st], ((j / FwdSmem::kStages) & 1) ^ 1)) {
+      for (int j = FwdSmem::kStages; j < nkv; ++j) {
+        if (!mbar_wait(&kv_empty[j % FwdSmem::kStages], ((j / FwdSmem::kStages) & 1) ^ 1)) {
           atomicOr(err, kErrWaitProducer);
-          ok = false;
+          // wait for the copies in flight before the CTA's shared memory goes
+          mbar_wait(q_full, 0);
+          for (int i = j - FwdSmem::kStages; i < j; ++i)
+            mbar_wait(&kv_full[i % FwdSmem::kStages], (i / FwdSmem::kStages) & 1);
           break;
         }
-        uint8_t* dst = smem + FwdSmem::KV + st * 2 * kTileBytes;
-        mbar_arrive_expect_tx(&kv_full[st], 2 * kTileBytes);
-        tma_load_3d(dst, &tmK, &kv_full[st], h * kHd, j * kSub, b);
-        tma_load_3d(dst + kTileBytes, &tmV, &kv_full[st], h * kHd, j * kSub, b);
-        issued = j + 1;
-      }
-      if (!ok) {  // wait for the copies in flight before the CTA's shared memory goes
-        mbar_wait(q_full, 0);
-        for (int j = issued > FwdSmem::kStages ? issued - FwdSmem::kStages : 0; j < issued; ++j)
-          mbar_wait(&kv_full[j % FwdSmem::kStages], (j / FwdSmem::kStages) & 1);
+        load_tile(j);
       }
     }
   } else if (warp == 5) {
@@ -774,7 +777,6 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
   const int64_t bh = static_cast<int64_t>(b) * a.H + h;
   const int n_sub = (len + kSub - 1) / kSub;
   if (tile * 128 >= len) {  // padded rows, in a batch that is taken as it comes or (own statistics) an empty clip
-    if (threadIdx.x == 0) pdl_launch_dependents();
     if (a.dout) {
       const int64_t at = b * a.g.bs + h * kHd;
       zero_rows((KEYS ? a.g.dk : a.g.dq) + at, a.g.ld, 0, a.T);
@@ -783,7 +785,22 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
     return;
   }
 
-  if (threadIdx.x == 0) {
+  auto load_tile = [&](int j) {
+    const int st = j % BwdSmem::kStages;
+    uint8_t* dst = smem + BwdSmem::B + st * 2 * kTileBytes;
+    mbar_arrive_expect_tx(&b_full[st], 2 * kTileBytes + (KEYS && !a.dout ? 2 * BwdSmem::kAugTile : 0));
+    tma_load_3d(dst, &tmB1, &b_full[st], h * kHd, j * kSub, b);
+    tma_load_3d(dst + kTileBytes, &tmB2, &b_full[st], h * kHd, j * kSub, b);
+    if (KEYS && !a.dout) {
+      uint8_t* aug = smem + BwdSmem::AugB + st * 2 * BwdSmem::kAugTile;
+      const int64_t at = bh * a.tiles * 128 * kAugRow + j * BwdSmem::kAugTile;
+      bulk_load(aug, a.aug_l + at, BwdSmem::kAugTile, &b_full[st]);
+      bulk_load(aug + BwdSmem::kAugTile, a.aug_d + at, BwdSmem::kAugTile, &b_full[st]);
+    }
+  };
+  // The copying thread sets up the barriers and starts the first copies before the
+  // others have the tensor memory.
+  if (threadIdx.x == 8 * 32) {
     mbar_init(a_full, 1);
     mbar_init(s_read, 8);
     mbar_init(s_full, 1);
@@ -795,7 +812,18 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
       mbar_init(&b_empty[i], 1);
     }
     fence_mbar_init();
-    pdl_launch_dependents();
+    fence_proxy_async_smem();
+    mbar_arrive_expect_tx(a_full, 4 * kTileBytes + (KEYS || a.dout ? 0 : 2 * 128 * kAugRow));
+    for (int i = 0; i < 2; ++i) {
+      tma_load_3d(smem + BwdSmem::A + i * kTileBytes, &tmA1, a_full, h * kHd, tile * 128 + i * kSub, b);
+      tma_load_3d(smem + BwdSmem::A + (2 + i) * kTileBytes, &tmA2, a_full, h * kHd, tile * 128 + i * kSub, b);
+    }
+    if (!KEYS && !a.dout) {
+      const int64_t at = (bh * a.tiles + tile) * 128 * kAugRow;
+      bulk_load(smem + BwdSmem::AugA, a.aug_l + at, 128 * kAugRow, a_full);
+      bulk_load(smem + BwdSmem::AugA + 128 * kAugRow, a.aug_d + at, 128 * kAugRow, a_full);
+    }
+    for (int j = 0; j < min(n_sub, BwdSmem::kStages); ++j) load_tile(j);
   }
   if (warp == 9) {
     tmem_alloc(tmem_slot, 256);
@@ -810,7 +838,6 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
   }
   int e = 0;  // of dS's scale (see below)
   if (a.dout) {
-    if (!a.frames) pdl_wait();
     e = own_statistics<BF16, KEYS>(a, smem, b, h, len);
   }
   fence_proxy_async_smem();
@@ -820,45 +847,20 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
   const uint32_t tmem = uniform(*tmem_slot);
   // dV (key CTA) | dK or dQ | S | dP, then dS and P
   const uint32_t tAcc1 = tmem, tAcc2 = tmem + 64, tS = tmem + 128, tD = tmem + 192;
-  if (!a.frames && !a.dout) pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
 
   if (warp == 8) {
     if (lane == 0) {
-      mbar_arrive_expect_tx(a_full, 4 * kTileBytes + (KEYS || a.dout ? 0 : 2 * 128 * kAugRow));
-      for (int i = 0; i < 2; ++i) {
-        tma_load_3d(smem + BwdSmem::A + i * kTileBytes, &tmA1, a_full, h * kHd, tile * 128 + i * kSub, b);
-        tma_load_3d(smem + BwdSmem::A + (2 + i) * kTileBytes, &tmA2, a_full, h * kHd, tile * 128 + i * kSub, b);
-      }
-      const uint8_t* al = a.aug_l + bh * a.tiles * 128 * kAugRow;
-      const uint8_t* ad = a.aug_d + bh * a.tiles * 128 * kAugRow;
-      if (!KEYS && !a.dout) {
-        bulk_load(smem + BwdSmem::AugA, al + tile * 128 * kAugRow, 128 * kAugRow, a_full);
-        bulk_load(smem + BwdSmem::AugA + 128 * kAugRow, ad + tile * 128 * kAugRow, 128 * kAugRow, a_full);
-      }
-      int issued = 0;
-      bool ok = true;
-      for (int j = 0; j < n_sub; ++j) {
-        const int st = j % BwdSmem::kStages;
-        if (j >= BwdSmem::kStages && !mbar_wait(&b_empty[st], ((j / BwdSmem::kStages) & 1) ^ 1)) {
+      for (int j = BwdSmem::kStages; j < n_sub; ++j) {
+        if (!mbar_wait(&b_empty[j % BwdSmem::kStages], ((j / BwdSmem::kStages) & 1) ^ 1)) {
           atomicOr(a.err, kErrWaitProducer);
-          ok = false;
+          // wait for the copies in flight before the CTA's shared memory goes
+          mbar_wait(a_full, 0);
+          for (int i = j - BwdSmem::kStages; i < j; ++i)
+            mbar_wait(&b_full[i % BwdSmem::kStages], (i / BwdSmem::kStages) & 1);
           break;
         }
-        uint8_t* dst = smem + BwdSmem::B + st * 2 * kTileBytes;
-        mbar_arrive_expect_tx(&b_full[st], 2 * kTileBytes + (KEYS && !a.dout ? 2 * BwdSmem::kAugTile : 0));
-        tma_load_3d(dst, &tmB1, &b_full[st], h * kHd, j * kSub, b);
-        tma_load_3d(dst + kTileBytes, &tmB2, &b_full[st], h * kHd, j * kSub, b);
-        if (KEYS && !a.dout) {
-          uint8_t* aug = smem + BwdSmem::AugB + st * 2 * BwdSmem::kAugTile;
-          bulk_load(aug, al + j * BwdSmem::kAugTile, BwdSmem::kAugTile, &b_full[st]);
-          bulk_load(aug + BwdSmem::kAugTile, ad + j * BwdSmem::kAugTile, BwdSmem::kAugTile, &b_full[st]);
-        }
-        issued = j + 1;
-      }
-      if (!ok) {  // wait for the copies in flight before the CTA's shared memory goes
-        mbar_wait(a_full, 0);
-        for (int j = issued > BwdSmem::kStages ? issued - BwdSmem::kStages : 0; j < issued; ++j)
-          mbar_wait(&b_full[j % BwdSmem::kStages], (j / BwdSmem::kStages) & 1);
+        load_tile(j);
       }
     }
   } else if (warp == 9) {
@@ -1048,10 +1050,8 @@ attention_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   // In this order: key CTAs (the longer ones) and query CTAs of tiles with frames,
   // and CTAs with nothing to do (the grid is for full clips).
   int live = a.tiles * a.batch * a.H;
-  if (a.frames) {
-    pdl_wait();
-    live = live_units(a.frames, a.batch, a.T, a.H, live, threadIdx.x & 31);
-  }
+  pdl_wait();  // before tensor memory is asked for, as in the forward kernel
+  if (a.frames) live = live_units(a.frames, a.batch, a.T, a.H, live, threadIdx.x & 31);
   // (with its own statistics the kernel also writes the zeros of empty clips: there
   // the units without frames follow, key units first)
   const int u = blockIdx.x, units = a.tiles * a.batch * a.H;

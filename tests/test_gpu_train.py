@@ -354,6 +354,35 @@ def test_attention_forward_agrees_with_the_inference_kernel():
     assert (ref.float() - out.float()).abs().max() <= 8 * 2.0 ** -11 * float(v.abs().max())
 
 
+def test_attention_in_a_row_with_the_inference_kernels():
+    """Kernels that start early behind one another and all want tensor memory: the inference attention (all of it),
+    a GEMM, both training passes, in one queue."""
+    gen = torch.Generator().manual_seed(21)
+    T, H, t_pad = 700, 4, 704
+    t3 = _rand(gen, 1, T, 3, H * 64).half()
+    q, k, v = _triple(t3, "dense")
+    vt = torch.zeros(1, H, 64, t_pad, dtype=F16, device="cuda")
+    vt[..., :T] = v.unflatten(2, (H, 64)).permute(0, 2, 3, 1)
+    do = _rand(gen, 1, T, H * 64, std=0.1).half().cuda()
+    W = _rand(gen, H * 64, H * 64, std=0.1).half().cuda()
+    err = _err()
+
+    def queue():
+        inf, out, gemm = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+        lse, grads = torch.empty(1, H, T, device="cuda"), [torch.empty_like(q) for _ in range(3)]
+        assert B.w2v_op_attention(q, k, vt, inf, 1, T, H, t_pad, err) == 0
+        B.w2v_op_attention_fwd(q, k, v, out, lse, err)
+        assert B.w2v_op_gemm(out, W, T, H * 64, H * 64, None, None, 0, gemm, 0, 0, err) == 0
+        B.w2v_op_attention_bwd(do, q, k, v, out, lse, *grads, err)
+        return inf, out, gemm, *grads
+
+    runs = [queue() for _ in range(30)]
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for r in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(r, runs[0]))
+
+
 # ------------------------------------------------------------------ LayerNorm
 
 LN_TYPES = [(F16, F16), (BF16, BF16), (F32, F32), (F32, F16), (F32, BF16)]
