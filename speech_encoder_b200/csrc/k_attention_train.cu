@@ -514,6 +514,44 @@ __device__ __forceinline__ uint4 aug_pieces(float v, bool rowsum, int half) {
                     pack2<BF16>(ch[6], ch[7]));
 }
 
+// A row's rowsum(dout o out) for a clip of few frames, recomputed from its
+// probabilities: sum_j P_j dP_j / sum_j P_j.  Where one key has nearly all of a row's
+// weight, dP - rowsum is a small difference, and the rounding of out in the row sum
+// may be all of it: with 2 frames in bf16 dq came out wrong by its own size in the
+// worst of 2000 draws, with 8 by 1 %, with 24 by 0.6 %, and from 32 on within the
+// rounding of dS.  Eight neighbouring threads share a row, with 8 channels of its q
+// and dout each (and k, v at those channels); all threads of the warp take part.
+constexpr int kShortClip = 32;
+template <bool BF16>
+__device__ __forceinline__ float exact_row_sum(uint4 q, uint4 dout, const uint16_t* k, const uint16_t* v, int64_t ld,
+                                               int len, float lse) {
+  const uint32_t qu[4] = {q.x, q.y, q.z, q.w}, du[4] = {dout.x, dout.y, dout.z, dout.w};
+  float sum = 0.f, total = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < len; ++j) {
+    const uint4 k4 = *reinterpret_cast<const uint4*>(k + j * ld);
+    const uint4 v4 = *reinterpret_cast<const uint4*>(v + j * ld);
+    const uint32_t ku[4] = {k4.x, k4.y, k4.z, k4.w}, vu[4] = {v4.x, v4.y, v4.z, v4.w};
+    float s = 0.f, dp = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = unpack2<BF16>(qu[i]), b = unpack2<BF16>(ku[i]);
+      const float2 x = unpack2<BF16>(du[i]), y = unpack2<BF16>(vu[i]);
+      s = fmaf(a.x, b.x, fmaf(a.y, b.y, s));
+      dp = fmaf(x.x, y.x, fmaf(x.y, y.y, dp));
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      dp += __shfl_xor_sync(0xffffffffu, dp, o);
+    }
+    const float p = ex2_approx(fmaf(s, kC2, -lse * kLog2e));
+    sum = fmaf(p, dp, sum);
+    total += p;
+  }
+  return sum / total;
+}
+
 struct BwdOut {
   uint16_t* dq;
   uint16_t* dk;
@@ -523,11 +561,13 @@ struct BwdOut {
 
 // In fp16 also, per 128 frames, the largest |dout row|^2 and |v row|^2.  Tiles of
 // padded rows alone get their zero gradients here.
-// Eight lanes a row, 16 bytes each.
+// Eight lanes a row, 16 bytes each.  Three blocks an SM: two cost 0.9 us of 22.0 at
+// 1499 frames x 12 heads, and four spill registers.
 template <bool BF16>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
 attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ out, int64_t out_ld,
-                          int64_t out_bs, const uint16_t* __restrict__ v, int64_t v_ld, int64_t v_bs,
+                          int64_t out_bs, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
+                          const uint16_t* __restrict__ v, int64_t qkv_ld, int64_t qkv_bs,
                           const float* __restrict__ lse, const int32_t* __restrict__ frames, int T, int H, int tiles,
                           uint8_t* __restrict__ aug_l, uint8_t* __restrict__ aug_d, float2* __restrict__ peak,
                           const BwdOut g) {
@@ -559,7 +599,7 @@ attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __r
       const int64_t at = b * out_bs + t * out_ld + h * kHd + part * 8;
       ra[it] = *reinterpret_cast<const uint4*>(dout + at);
       ro[it] = *reinterpret_cast<const uint4*>(out + at);
-      if (!BF16) rv[it] = *reinterpret_cast<const uint4*>(v + b * v_bs + t * v_ld + h * kHd + part * 8);
+      if (!BF16) rv[it] = *reinterpret_cast<const uint4*>(v + b * qkv_bs + t * qkv_ld + h * kHd + part * 8);
       rl[it] = lse[static_cast<int64_t>(bh) * T + t];
     }
   }
@@ -590,9 +630,15 @@ attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __r
       top_do = fmaxf(top_do, ndo);
       top_v = fmaxf(top_v, nv);
     }
+    if (len <= kShortClip && it == 0) {  // (all its rows are among the first)
+      const int64_t head = b * qkv_bs + h * kHd + part * 8;
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      const uint4 q4 = t < len ? *reinterpret_cast<const uint4*>(q + head + t * qkv_ld) : none;
+      d = exact_row_sum<BF16>(q4, ra[0], k + head, v + head, qkv_ld, len, t < len ? rl[0] : 0.f);
+    }
     if (part < 4) {
       const bool rowsum = part >= 2;
-      const float value = rowsum ? -d : (rl[it] == -INFINITY ? -INFINITY : -8.0f * rl[it]);
+      const float value = rowsum ? (t < len ? -d : 0.f) : (rl[it] == -INFINITY ? -INFINITY : -8.0f * rl[it]);
       uint8_t* dst = (rowsum ? aug_d : aug_l) + (static_cast<int64_t>(bh) * tiles + tile) * 128 * kAugRow;
       *reinterpret_cast<uint4*>(dst + aug_offset(it * 32 + (threadIdx.x >> 3), part & 1)) =
           aug_pieces<BF16>(value, rowsum, part & 1);
@@ -686,9 +732,11 @@ struct BwdArgs {
   // launch, against 8.0 and two); null otherwise.
   const uint16_t* dout;
   const uint16_t* out;
+  const uint16_t* q;
+  const uint16_t* k;
   const uint16_t* v;
   const float* lse;
-  int64_t out_ld, out_bs, v_ld, v_bs;
+  int64_t out_ld, out_bs, qkv_ld, qkv_bs;
 };
 
 // The statistics of one clip of at most 128 frames, as attention_bwd_rows_kernel
@@ -703,7 +751,7 @@ __device__ __forceinline__ int own_statistics(const BwdArgs& a, uint8_t* smem, i
     float d = 0.f, l = -INFINITY;
     if (row < len) {
       const int64_t at = b * a.out_bs + row * a.out_ld + h * kHd + part * 32;
-      const int64_t va = b * a.v_bs + row * a.v_ld + h * kHd + part * 32;
+      const int64_t va = b * a.qkv_bs + row * a.qkv_ld + h * kHd + part * 32;
 #pragma unroll
       for (int c = 0; c < 32; c += 8) {
         const uint4 x4 = *reinterpret_cast<const uint4*>(a.dout + at + c);
@@ -729,9 +777,25 @@ __device__ __forceinline__ int own_statistics(const BwdArgs& a, uint8_t* smem, i
     uint8_t* dst = KEYS ? smem + BwdSmem::AugB + (row >> 6) * 2 * BwdSmem::kAugTile + part * BwdSmem::kAugTile
                         : smem + BwdSmem::AugA + part * 128 * kAugRow;
     const int at = KEYS ? row & 63 : row;
+    if (part == 0 || row >= kShortClip || len > kShortClip) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
-      *reinterpret_cast<uint4*>(dst + aug_offset(at, half)) = aug_pieces<BF16>(value, part, half);
+      for (int half = 0; half < 2; ++half)
+        *reinterpret_cast<uint4*>(dst + aug_offset(at, half)) = aug_pieces<BF16>(value, part, half);
+    }
+    if (len <= kShortClip) {  // the other row sums: eight threads a row
+      const int i = threadIdx.x >> 3, c = threadIdx.x & 7;
+      const int64_t head = b * a.qkv_bs + h * kHd + c * 8;
+      uint4 q4 = make_uint4(0, 0, 0, 0), d4 = q4;
+      float lse = 0.f;
+      if (i < len) {
+        q4 = *reinterpret_cast<const uint4*>(a.q + head + i * a.qkv_ld);
+        d4 = *reinterpret_cast<const uint4*>(a.dout + b * a.out_bs + i * a.out_ld + h * kHd + c * 8);
+        lse = a.lse[(static_cast<int64_t>(b) * a.H + h) * a.T + i];
+      }
+      const float sum = exact_row_sum<BF16>(q4, d4, a.k + head, a.v + head, a.qkv_ld, len, lse);
+      uint8_t* to = KEYS ? smem + BwdSmem::AugB + BwdSmem::kAugTile : smem + BwdSmem::AugA + 128 * kAugRow;
+      if (c < 2) *reinterpret_cast<uint4*>(to + aug_offset(i, c)) = aug_pieces<BF16>(i < len ? -sum : 0.f, 1, c);
+    }
     if (!BF16) {
       top_do += __shfl_xor_sync(0xffffffffu, top_do, 1);
       top_v += __shfl_xor_sync(0xffffffffu, top_v, 1);
@@ -1114,16 +1178,18 @@ cudaError_t launch_attention_bwd(const AttnTrain& s, const void* dout, const voi
   const bool own = tiles == 1;
   if (!own) {
     r = launch_pdl(s.bf16 ? attention_bwd_rows_kernel<true> : attention_bwd_rows_kernel<false>, dim3(tiles * bh),
-                   dim3(256), 0, st, u16(dout), u16(out), s.out_ld, s.out_bs, u16(v), s.qkv_ld, s.qkv_bs, lse,
+                   dim3(256), 0, st, u16(dout), u16(out), s.out_ld, s.out_bs, u16(q), u16(k), u16(v), s.qkv_ld, s.qkv_bs, lse,
                    s.frames, s.T, s.H, tiles, aug_l, aug_d, peak, a.g);
     if (r != cudaSuccess) return r;
   }
   a.dout = own ? u16(dout) : nullptr;
   a.out = u16(out);
+  a.q = u16(q);
+  a.k = u16(k);
   a.v = u16(v);
   a.lse = lse;
   a.out_ld = s.out_ld; a.out_bs = s.out_bs;
-  a.v_ld = s.qkv_ld; a.v_bs = s.qkv_bs;
+  a.qkv_ld = s.qkv_ld; a.qkv_bs = s.qkv_bs;
   a.frames = s.frames;
   a.aug_l = aug_l;
   a.aug_d = aug_d;

@@ -54,7 +54,9 @@ def attention(q, k, v, H, frames=None, dout=None, out_saved=None):
                 continue
             do, os = dout[at].double(), out_saved[at].double()
             dv = p.T @ do
-            dp, rows = do @ vd.T, (do * os).sum(1, keepdim=True)
+            dp = do @ vd.T
+            # short clips: the row sum from the probabilities, not from the rounded out
+            rows = ((p * dp) if n <= 32 else (do * os)).sum(1, keepdim=True)
             ds = p * (dp - rows)
             mag = p * (do.abs() @ vd.abs().T + (do * os).abs().sum(1, keepdim=True))
             if n == 1:
