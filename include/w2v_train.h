@@ -65,9 +65,9 @@ size_t w2v_op_attention_bwd_workspace(int batch, int T, int H);
  *   dq = dS k / 8,  dk = dS^T q / 8.
  * out and lse are the forward call's.  dq, dk and dv are overwritten, with
  * zeros past a clip's frames; dout, like the other inputs, is not used there.
- * For clips of up to 32 frames the row sum is recomputed as sum_j P_j dP_j, since
- * the rounding of out would be most of what is left of dP - rowsum in rows where
- * one key has nearly all the weight.
+ * The rounding of out in the row sum leaves an error in proportion to P in dS; dq has
+ * it taken out again (what a row of dS sums to, times P k), and in clips of up to 64
+ * frames dk too.
  * P and dS are rounded to dtype for the products (dS, in fp16, after scaling by
  * a power of two per clip and head that keeps it in range); everything else is
  * fp32.  No atomics.  Errors as above, and W2V_EINVAL if ws_bytes is too

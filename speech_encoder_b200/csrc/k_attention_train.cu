@@ -192,6 +192,28 @@ __device__ __forceinline__ void stage_row_part(uint32_t taddr, uint8_t* tile, in
   }
 }
 
+// The same of acc1 - w acc2.
+template <bool BF16>
+__device__ __forceinline__ void stage_row_difference(uint32_t acc1, uint32_t acc2, uint8_t* tile, int r, int c0,
+                                                     float scale, float w, bool live) {
+#pragma unroll
+  for (int half = 0; half < 32; half += 16) {
+    float v[16], x[16];
+    tmem_ld16(acc1 + half, v);
+    tmem_ld16(acc2 + half, x);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = scale * fmaf(-w, x[i], v[i]);
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (live)
+        u = make_uint4(pack2<BF16>(v[i], v[i + 1]), pack2<BF16>(v[i + 2], v[i + 3]), pack2<BF16>(v[i + 4], v[i + 5]),
+                       pack2<BF16>(v[i + 6], v[i + 7]));
+      *reinterpret_cast<uint4*>(tile + swizzled(r, c0 + (half + i) / 8)) = u;
+    }
+  }
+}
+
 // A staged tile to rows [0, rows) of one head, eight threads a row (a thread per
 // row, straight from its registers, writes 32 lines an instruction and took 2.3 us
 // for two tiles where this takes 1.5).
@@ -514,44 +536,6 @@ __device__ __forceinline__ uint4 aug_pieces(float v, bool rowsum, int half) {
                     pack2<BF16>(ch[6], ch[7]));
 }
 
-// A row's rowsum(dout o out) for a clip of few frames, recomputed from its
-// probabilities: sum_j P_j dP_j / sum_j P_j.  Where one key has nearly all of a row's
-// weight, dP - rowsum is a small difference, and the rounding of out in the row sum
-// may be all of it: with 2 frames in bf16 dq came out wrong by its own size in the
-// worst of 2000 draws, with 8 by 1 %, with 24 by 0.6 %, and from 32 on within the
-// rounding of dS.  Eight neighbouring threads share a row, with 8 channels of its q
-// and dout each (and k, v at those channels); all threads of the warp take part.
-constexpr int kShortClip = 32;
-template <bool BF16>
-__device__ __forceinline__ float exact_row_sum(uint4 q, uint4 dout, const uint16_t* k, const uint16_t* v, int64_t ld,
-                                               int len, float lse) {
-  const uint32_t qu[4] = {q.x, q.y, q.z, q.w}, du[4] = {dout.x, dout.y, dout.z, dout.w};
-  float sum = 0.f, total = 0.f;
-#pragma unroll 1
-  for (int j = 0; j < len; ++j) {
-    const uint4 k4 = *reinterpret_cast<const uint4*>(k + j * ld);
-    const uint4 v4 = *reinterpret_cast<const uint4*>(v + j * ld);
-    const uint32_t ku[4] = {k4.x, k4.y, k4.z, k4.w}, vu[4] = {v4.x, v4.y, v4.z, v4.w};
-    float s = 0.f, dp = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 a = unpack2<BF16>(qu[i]), b = unpack2<BF16>(ku[i]);
-      const float2 x = unpack2<BF16>(du[i]), y = unpack2<BF16>(vu[i]);
-      s = fmaf(a.x, b.x, fmaf(a.y, b.y, s));
-      dp = fmaf(x.x, y.x, fmaf(x.y, y.y, dp));
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      dp += __shfl_xor_sync(0xffffffffu, dp, o);
-    }
-    const float p = ex2_approx(fmaf(s, kC2, -lse * kLog2e));
-    sum = fmaf(p, dp, sum);
-    total += p;
-  }
-  return sum / total;
-}
-
 struct BwdOut {
   uint16_t* dq;
   uint16_t* dk;
@@ -561,13 +545,11 @@ struct BwdOut {
 
 // In fp16 also, per 128 frames, the largest |dout row|^2 and |v row|^2.  Tiles of
 // padded rows alone get their zero gradients here.
-// Eight lanes a row, 16 bytes each.  Three blocks an SM: two cost 0.9 us of 22.0 at
-// 1499 frames x 12 heads, and four spill registers.
+// Eight lanes a row, 16 bytes each.
 template <bool BF16>
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(256)
 attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __restrict__ out, int64_t out_ld,
-                          int64_t out_bs, const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
-                          const uint16_t* __restrict__ v, int64_t qkv_ld, int64_t qkv_bs,
+                          int64_t out_bs, const uint16_t* __restrict__ v, int64_t v_ld, int64_t v_bs,
                           const float* __restrict__ lse, const int32_t* __restrict__ frames, int T, int H, int tiles,
                           uint8_t* __restrict__ aug_l, uint8_t* __restrict__ aug_d, float2* __restrict__ peak,
                           const BwdOut g) {
@@ -599,7 +581,7 @@ attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __r
       const int64_t at = b * out_bs + t * out_ld + h * kHd + part * 8;
       ra[it] = *reinterpret_cast<const uint4*>(dout + at);
       ro[it] = *reinterpret_cast<const uint4*>(out + at);
-      if (!BF16) rv[it] = *reinterpret_cast<const uint4*>(v + b * qkv_bs + t * qkv_ld + h * kHd + part * 8);
+      if (!BF16) rv[it] = *reinterpret_cast<const uint4*>(v + b * v_bs + t * v_ld + h * kHd + part * 8);
       rl[it] = lse[static_cast<int64_t>(bh) * T + t];
     }
   }
@@ -630,15 +612,9 @@ attention_bwd_rows_kernel(const uint16_t* __restrict__ dout, const uint16_t* __r
       top_do = fmaxf(top_do, ndo);
       top_v = fmaxf(top_v, nv);
     }
-    if (len <= kShortClip && it == 0) {  // (all its rows are among the first)
-      const int64_t head = b * qkv_bs + h * kHd + part * 8;
-      const uint4 none = make_uint4(0, 0, 0, 0);
-      const uint4 q4 = t < len ? *reinterpret_cast<const uint4*>(q + head + t * qkv_ld) : none;
-      d = exact_row_sum<BF16>(q4, ra[0], k + head, v + head, qkv_ld, len, t < len ? rl[0] : 0.f);
-    }
     if (part < 4) {
       const bool rowsum = part >= 2;
-      const float value = rowsum ? (t < len ? -d : 0.f) : (rl[it] == -INFINITY ? -INFINITY : -8.0f * rl[it]);
+      const float value = rowsum ? -d : (rl[it] == -INFINITY ? -INFINITY : -8.0f * rl[it]);
       uint8_t* dst = (rowsum ? aug_d : aug_l) + (static_cast<int64_t>(bh) * tiles + tile) * 128 * kAugRow;
       *reinterpret_cast<uint4*>(dst + aug_offset(it * 32 + (threadIdx.x >> 3), part & 1)) =
           aug_pieces<BF16>(value, rowsum, part & 1);
@@ -689,6 +665,20 @@ __device__ __forceinline__ int ds_exponent(const float2* peak, int tiles, int la
 }
 
 // ------------------------------------------------------------------- backward
+// Sums over the warp of 16 values a lane: every two lanes get one value's, in order.
+__device__ __forceinline__ float column_sums(float (&v)[16], int lane) {
+#pragma unroll
+  for (int n = 8; n >= 1; n >>= 1) {
+    const bool up = lane & (2 * n);
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], 2 * n);
+      v[i] = (up ? v[i + n] : v[i]) + other;
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
 // Two kinds of CTA in one launch, with the same inner step.  A CTA holds 128
 // rows of a pair of operands (A1, A2) and streams 64-row tiles of the other
 // pair (B1, B2), each with its 16 statistics channels; per tile
@@ -697,8 +687,16 @@ __device__ __forceinline__ int ds_exponent(const float2* peak, int tiles, int la
 // A key CTA holds (K, V) and streams (Q, dO); its S, P and dS are transposed
 // (row = key) and, rounded to the operand type, the A operands of
 //   dV += P dO, dK += dS Q                 (M = 128, N = 64, K = 64 queries).
-// A query CTA holds (Q, dO), streams (K, V) and needs only dQ += dS K.  S and dP
-// are computed twice, which costs 7 products instead of the 5 of a single pass,
+// A query CTA holds (Q, dO), streams (K, V) and sums dQ += dS K and P K.  A row of dS
+// sums to zero; what the rounded one sums to, r, is the error of rowsum(dO o out),
+// from the rounding of out, and of its own entries' roundings, all nearly in proportion to
+// P: so dQ - r (P K) is what it writes.  dq is then off by 1.31-1.36 times one rounding
+// of the exact result, and was by 1.53-1.66 without, at 49 to 2999 frames; 2 x 2999
+// frames x 16 heads take 315 us for 288, 799 x 12 25.4 for 22.8.  dk has the error of
+// the row sums of other CTAs' rows and stays at 1.44-1.6; in a clip of one tile of 64,
+// where it can be many times that, both kinds of CTA see whole rows of P o dP and take
+// their sum off first (49 x 12: 6.6 us for 5.9; dk 1.42 for 1.6).  S and dP
+// are computed twice, which costs 8 products instead of the 5 of a single pass,
 // but each gradient has one owner that sums it in a fixed order: no atomics and no
 // fp32 partial sums in memory.
 //
@@ -728,15 +726,13 @@ struct BwdArgs {
   int T, H, batch, tiles;
   int* err;
   // For T <= 128 a CTA makes the statistics of its clip itself (they are one tile's)
-  // and no other kernel runs before this one (49 frames x 12 heads: 5.9 us and one
-  // launch, against 8.0 and two); null otherwise.
+  // and no other kernel runs before this one (49 frames x 12 heads: one launch and
+  // 2 us less); null otherwise.
   const uint16_t* dout;
   const uint16_t* out;
-  const uint16_t* q;
-  const uint16_t* k;
   const uint16_t* v;
   const float* lse;
-  int64_t out_ld, out_bs, qkv_ld, qkv_bs;
+  int64_t out_ld, out_bs, v_ld, v_bs;
 };
 
 // The statistics of one clip of at most 128 frames, as attention_bwd_rows_kernel
@@ -751,7 +747,7 @@ __device__ __forceinline__ int own_statistics(const BwdArgs& a, uint8_t* smem, i
     float d = 0.f, l = -INFINITY;
     if (row < len) {
       const int64_t at = b * a.out_bs + row * a.out_ld + h * kHd + part * 32;
-      const int64_t va = b * a.qkv_bs + row * a.qkv_ld + h * kHd + part * 32;
+      const int64_t va = b * a.v_bs + row * a.v_ld + h * kHd + part * 32;
 #pragma unroll
       for (int c = 0; c < 32; c += 8) {
         const uint4 x4 = *reinterpret_cast<const uint4*>(a.dout + at + c);
@@ -777,25 +773,9 @@ __device__ __forceinline__ int own_statistics(const BwdArgs& a, uint8_t* smem, i
     uint8_t* dst = KEYS ? smem + BwdSmem::AugB + (row >> 6) * 2 * BwdSmem::kAugTile + part * BwdSmem::kAugTile
                         : smem + BwdSmem::AugA + part * 128 * kAugRow;
     const int at = KEYS ? row & 63 : row;
-    if (part == 0 || row >= kShortClip || len > kShortClip) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
-        *reinterpret_cast<uint4*>(dst + aug_offset(at, half)) = aug_pieces<BF16>(value, part, half);
-    }
-    if (len <= kShortClip) {  // the other row sums: eight threads a row
-      const int i = threadIdx.x >> 3, c = threadIdx.x & 7;
-      const int64_t head = b * a.qkv_bs + h * kHd + c * 8;
-      uint4 q4 = make_uint4(0, 0, 0, 0), d4 = q4;
-      float lse = 0.f;
-      if (i < len) {
-        q4 = *reinterpret_cast<const uint4*>(a.q + head + i * a.qkv_ld);
-        d4 = *reinterpret_cast<const uint4*>(a.dout + b * a.out_bs + i * a.out_ld + h * kHd + c * 8);
-        lse = a.lse[(static_cast<int64_t>(b) * a.H + h) * a.T + i];
-      }
-      const float sum = exact_row_sum<BF16>(q4, d4, a.k + head, a.v + head, a.qkv_ld, len, lse);
-      uint8_t* to = KEYS ? smem + BwdSmem::AugB + BwdSmem::kAugTile : smem + BwdSmem::AugA + 128 * kAugRow;
-      if (c < 2) *reinterpret_cast<uint4*>(to + aug_offset(i, c)) = aug_pieces<BF16>(i < len ? -sum : 0.f, 1, c);
-    }
+    for (int half = 0; half < 2; ++half)
+      *reinterpret_cast<uint4*>(dst + aug_offset(at, half)) = aug_pieces<BF16>(value, part, half);
     if (!BF16) {
       top_do += __shfl_xor_sync(0xffffffffu, top_do, 1);
       top_v += __shfl_xor_sync(0xffffffffu, top_v, 1);
@@ -909,7 +889,7 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
-  // dV (key CTA) | dK or dQ | S | dP, then dS and P
+  // dV or P K | dK or dQ | S | dP, then dS and P
   const uint32_t tAcc1 = tmem, tAcc2 = tmem + 64, tS = tmem + 128, tD = tmem + 192;
   if (threadIdx.x == 0) pdl_launch_dependents();
 
@@ -976,12 +956,10 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
         for (int kk = 0; kk < 4; ++kk)
           umma_f16_ts(tAcc2, tD + 32 * (kk >> 1) + 8 * (kk & 1), db1 + static_cast<uint64_t>(128 * kk), idG,
                       (j > 0 || kk > 0) ? 1u : 0u);
-        if (KEYS) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_f16_ts(tAcc1, tD + 16 + 32 * (kk >> 1) + 8 * (kk & 1), db2 + static_cast<uint64_t>(128 * kk), idG,
-                        (j > 0 || kk > 0) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16_ts(tAcc1, tD + 16 + 32 * (kk >> 1) + 8 * (kk & 1),
+                      (KEYS ? db2 : db1) + static_cast<uint64_t>(128 * kk), idG, (j > 0 || kk > 0) ? 1u : 0u);
         umma_commit(acc_done);
         umma_commit(&b_empty[j % BwdSmem::kStages]);
       }
@@ -1019,7 +997,9 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
     // shrinks dS is a factor of its own.
     if (!BF16 && !a.dout) e = ds_exponent(a.peak + bh * a.tiles, a.tiles, lane);
     const int up = max(0, min(15, e)), down = min(0, e);
+    const float unscale = exp2f(static_cast<float>(-up));
     const float shift = static_cast<float>(up), shrink = exp2f(static_cast<float>(down));
+    float2 left = make_float2(0.f, 0.f);  // query CTA: the sum of the row's dS as rounded
     bool ok = true;
     for (int j = 0; j < n_sub; ++j) {
       const int valid = len - j * kSub - half * 32;
@@ -1046,17 +1026,44 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
         for (int i = 0; i < 32; ++i)
           if (i >= valid) s[i] = 0.f;
       }
-      if (KEYS) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) pk[16 + i / 2] = pack2<BF16>(s[i], s[i + 1]);
-      }
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(dp_full, j & 1));
+      // A clip of one tile of 64 frames: what its rows of P o dP sum to is taken off dP
+      // before dS is rounded (in a longer clip only dQ is put right, at the end).
+      float* rest = reinterpret_cast<float*>(smem + BwdSmem::B + 2 * kTileBytes);  // (a stage that it does not use)
+      float own_rest = 0.f;
+      if (n_sub == 1) {
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < 32; c0 += 16) {
+            float g[16];
+            tmem_ld16(tD + lane_base + half * 32 + c0, g);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              g[i] = !KEYS || t < len ? g[i] * s[c0 + i] : 0.f;
+              if (!KEYS) own_rest += g[i];
+            }
+            if (KEYS) {
+              const float sum = column_sums(g, lane);
+              if (quarter < 2) rest[quarter * 64 + half * 32 + c0 + (lane >> 1)] = sum * unscale;
+            }
+          }
+          if (!KEYS) rest[half * 128 + row] = own_rest * unscale;
+        }
+        named_barrier_sync(1, 256);
+        if (!KEYS) own_rest = rest[row] + rest[128 + row];
+      }
       if (ok) {
         tc_fence_after();
 #pragma unroll
         for (int c0 = 0; c0 < 32; c0 += 16) {
           float dp[16];
           tmem_ld16(tD + lane_base + half * 32 + c0, dp);
+          if (n_sub == 1) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              dp[i] -= KEYS ? rest[half * 32 + c0 + i] + rest[64 + half * 32 + c0 + i] : own_rest;
+          }
           if (!BF16 && down < 0) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) dp[i] *= shrink;
@@ -1065,29 +1072,40 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
           for (int i = 0; i < 16; i += 2) {
             const float2 g = fmul2(make_float2(dp[i], dp[i + 1]), make_float2(s[c0 + i], s[c0 + i + 1]));
             pk[(c0 + i) / 2] = pack2<BF16>(g.x, g.y);
+            if (!KEYS) left = fadd2(left, unpack2<BF16>(pk[(c0 + i) / 2]));
           }
         }
         tmem_st16_u32(tD + lane_base + half * 32, *reinterpret_cast<const uint32_t(*)[16]>(pk));
-        if (KEYS)
-          tmem_st16_u32(tD + lane_base + half * 32 + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) pk[16 + i / 2] = pack2<BF16>(s[i], s[i + 1]);
+        tmem_st16_u32(tD + lane_base + half * 32 + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full);
     }
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(acc_done, (n_sub - 1) & 1));
+    if (!KEYS) {  // both column halves' sums of the row
+      float* sums = reinterpret_cast<float*>(smem + BwdSmem::A + 2 * kTileBytes);
+      if (ok) sums[half * 128 + row] = left.x + left.y;
+      named_barrier_sync(1, 256);
+      if (ok) left.x = sums[row] + sums[128 + row];
+    }
     if (ok) {
       tc_fence_after();
       const bool live = t < len;
       // A single frame has P = 1 and no gradient through the softmax: dP and
       // rowsum(dO o O) are the same number there, summed in two orders.
-      const float unscale = exp2f(static_cast<float>(-up));
       const float back = len == 1 ? 0.f : 0.125f * unscale * exp2f(static_cast<float>(-down));
       // over A1 and A2, which no product reads any more
-      stage_row_part<BF16>(tAcc2 + lane_base + half * 32, smem + BwdSmem::A, row, half * 4, back, live);
-      if (KEYS)
+      if (KEYS) {
+        stage_row_part<BF16>(tAcc2 + lane_base + half * 32, smem + BwdSmem::A, row, half * 4, back, live);
         stage_row_part<BF16>(tAcc1 + lane_base + half * 32, smem + BwdSmem::A + 2 * kTileBytes, row, half * 4, unscale,
                              live);
+      } else {
+        stage_row_difference<BF16>(tAcc2 + lane_base + half * 32, tAcc1 + lane_base + half * 32, smem + BwdSmem::A, row,
+                                   half * 4, back, left.x * unscale, live);
+      }
     } else if (lane == 0) {
       atomicOr(a.err, kErrWaitSoftmax);
     }
@@ -1178,18 +1196,16 @@ cudaError_t launch_attention_bwd(const AttnTrain& s, const void* dout, const voi
   const bool own = tiles == 1;
   if (!own) {
     r = launch_pdl(s.bf16 ? attention_bwd_rows_kernel<true> : attention_bwd_rows_kernel<false>, dim3(tiles * bh),
-                   dim3(256), 0, st, u16(dout), u16(out), s.out_ld, s.out_bs, u16(q), u16(k), u16(v), s.qkv_ld, s.qkv_bs, lse,
+                   dim3(256), 0, st, u16(dout), u16(out), s.out_ld, s.out_bs, u16(v), s.qkv_ld, s.qkv_bs, lse,
                    s.frames, s.T, s.H, tiles, aug_l, aug_d, peak, a.g);
     if (r != cudaSuccess) return r;
   }
   a.dout = own ? u16(dout) : nullptr;
   a.out = u16(out);
-  a.q = u16(q);
-  a.k = u16(k);
   a.v = u16(v);
   a.lse = lse;
   a.out_ld = s.out_ld; a.out_bs = s.out_bs;
-  a.qkv_ld = s.qkv_ld; a.qkv_bs = s.qkv_bs;
+  a.v_ld = s.qkv_ld; a.v_bs = s.qkv_bs;
   a.frames = s.frames;
   a.aug_l = aug_l;
   a.aug_d = aug_d;

@@ -55,17 +55,23 @@ def attention(q, k, v, H, frames=None, dout=None, out_saved=None):
             do, os = dout[at].double(), out_saved[at].double()
             dv = p.T @ do
             dp = do @ vd.T
-            # short clips: the row sum from the probabilities, not from the rounded out
-            rows = ((p * dp) if n <= 32 else (do * os)).sum(1, keepdim=True)
+            # clips of one tile: the row sum goes by the probabilities, not by the rounded out
+            rows = ((p * dp) if n <= 64 else (do * os)).sum(1, keepdim=True)
             ds = p * (dp - rows)
             mag = p * (do.abs() @ vd.abs().T + (do * os).abs().sum(1, keepdim=True))
             if n == 1:
                 ds = torch.zeros_like(ds)
-            dq, dk = ds @ kd / 8, ds.T @ qd / 8
+            # dq has what a row of the rounded dS sums to taken out again, in proportion to P: it goes by the exact
+            # row sum, and each rounding counts once with its key and once, at most, with the mean of the keys
+            exact = p * (dp - (p * dp).sum(1, keepdim=True)) if n > 1 else ds
+            dq, dk = exact @ kd / 8, ds.T @ qd / 8
             res["dv"][at], res["dq"][at], res["dk"][at] = dv, dq, dk
             tol["dv"][at] = u * dv.abs() + (u + FP32_SLACK) * (p.T @ do.abs()) + eps0
             each = u * ds.abs() + FP32_SLACK * mag
-            tol["dq"][at] = u * dq.abs() + each @ kd.abs() / 8 + eps0
+            mean = p @ kd.abs()
+            left = each.sum(1, keepdim=True) + (do * os).abs().sum(1, keepdim=True) * u
+            tol["dq"][at] = (u * dq.abs() + (each @ kd.abs() + each.sum(1, keepdim=True) * mean
+                                             + 2 * u * left * mean) / 8 + eps0)
             tol["dk"][at] = u * dk.abs() + each.T @ qd.abs() / 8 + eps0
     return res, tol, lse
 
