@@ -689,10 +689,10 @@ __device__ __forceinline__ float column_sums(float (&v)[16], int lane) {
 //   dV += P dO, dK += dS Q                 (M = 128, N = 64, K = 64 queries).
 // A query CTA holds (Q, dO), streams (K, V) and sums dQ += dS K and P K.  A row of dS
 // sums to zero; what the rounded one sums to, r, is the error of rowsum(dO o out),
-// from the rounding of out, and of its own entries' roundings, all nearly in proportion to
-// P: so dQ - r (P K) is what it writes.  dq is then off by 1.31-1.36 times one rounding
-// of the exact result, and was by 1.53-1.66 without, at 49 to 2999 frames; 2 x 2999
-// frames x 16 heads take 315 us for 288, 799 x 12 25.4 for 22.8.  dk has the error of
+// which has the rounding of out, and the sum of its own entries' roundings, all nearly
+// in proportion to P: so dQ - r (P K) is what it writes.  dq is then off by 1.31-1.36
+// times one rounding of the exact result, and was by 1.53-1.66 without, at 49 to 2999
+// frames; 2 x 2999 frames x 16 heads take 315 us for 288, 799 x 12 25.4 for 22.8.  dk has the error of
 // the row sums of other CTAs' rows and stays at 1.44-1.6; in a clip of one tile of 64,
 // where it can be many times that, both kinds of CTA see whole rows of P o dP and take
 // their sum off first (49 x 12: 6.6 us for 5.9; dk 1.42 for 1.6).  S and dP
