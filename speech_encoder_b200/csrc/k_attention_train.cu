@@ -1020,8 +1020,10 @@ __device__ __forceinline__ void bwd_body(const CUtensorMap& tmA1, const CUtensor
         s[i] = p.x;
         s[i + 1] = p.y;
       }
-      // Keys past the clip: their scores are -8 lse, not -infinity, and may overflow.
-      if (!KEYS && valid < 32) {
+      // Columns past the clip.  A query CTA's scores of such keys are -8 lse, not -infinity,
+      // and may overflow; a key CTA's of such queries are -infinity, but NaN where the key
+      // holds an infinity (times the zeros of the query), and NaN would reach dV and dK.
+      if (valid < 32) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (i >= valid) s[i] = 0.f;
