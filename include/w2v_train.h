@@ -49,6 +49,8 @@ typedef struct {
  * exponentials, which the backward pass recomputes the probabilities from.
  * Rows past a clip's frames are written: out 0, lse -infinity; what the inputs
  * hold there, NaN included, is not used.  err_dev as in w2v_ops.h.
+ * A row of a clip's own frames with a score that is NaN or +infinity, or with
+ * none above -infinity, has no softmax: its out and lse are NaN.
  * Scores, softmax and sums are fp32; the probabilities are rounded to dtype for
  * the product with v.
  * Errors: W2V_EINVAL (null or misaligned pointer, dtype, strides), W2V_ESHAPE

@@ -25,6 +25,7 @@ constexpr int kTileBytes = kSub * kHd * 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kC2 = 0.125f * kLog2e;  // scores to log2 units
+constexpr float kLowest = -3.402823466e38f;  // the lowest fp32: below every finite score in log2 units
 
 // kind::f16 instruction descriptor with an fp32 accumulator: A and B both fp16
 // or both bf16, A K-major (or in tensor memory), B K-major or MN-major.
@@ -141,7 +142,8 @@ __device__ __forceinline__ Unit find_unit(const int32_t* frames, int batch, int 
 // nearest integer (adding 1.5 * 2^23 leaves j in the low mantissa bits), 2^f by the
 // polynomial of degree 4 with the smallest largest relative error on [-1/2, 1/2]
 // (2.7e-6, found by linear programming over a fine grid), j added to the
-// exponent.  x is clamped below at -126.
+// exponent.  x is clamped below at -126, and so is NaN: rows with a score that is
+// not finite are found by their maximum (see the forward kernel).
 __device__ __forceinline__ float2 exp2_poly(float2 x) {
   constexpr float kMagic = 12582912.0f;
   x = make_float2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
@@ -377,7 +379,12 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   } else {
     const int r = warp * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-    float m_ref = -INFINITY, l = 0.f;  // reference maximum (log2 units), sum of exponentials
+    // Reference maximum (log2 units), sum of exponentials.  A row whose softmax is not
+    // defined ends with a reference that is not finite or still the lowest, and gets
+    // NaN: +infinity stands for a NaN or an infinite score, the lowest for a row without
+    // a score above -infinity.  The probabilities do not show it by themselves: the
+    // polynomial makes 2^-126 of NaN.
+    float m_ref = kLowest, l = 0.f;
     bool ok = true;
     for (int j = 0; j < nkv; ++j) {
       const uint32_t cols = tS + 64 * (j % 3) + lane_base;
@@ -397,14 +404,16 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
         for (int i = 4; i < kSub; i += 8) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = i + 4 < kSub ? fmax3(mx[k], s[i + k], s[i + 4 + k]) : fmaxf(mx[k], s[i + k]);
+          for (int k = 0; k < 4; ++k)
+            mx[k] = i + 4 < kSub ? fmax3_nan(mx[k], s[i + k], s[i + 4 + k]) : fmax_nan(mx[k], s[i + k]);
         }
-        mx[0] = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+        mx[0] = fmax3_nan(mx[0], mx[1], fmax_nan(mx[2], mx[3]));
         // The reference moves only when the maximum exceeds it by 2^8, so the
-        // accumulator is rarely rescaled and P stays <= 256.
-        const bool move = mx[0] * kC2 > m_ref + 8.0f;
+        // accumulator is rarely rescaled and P stays <= 256; for NaN it moves to
+        // +infinity, once.
+        const bool move = !(mx[0] * kC2 <= m_ref + 8.0f) && m_ref < INFINITY;
         if (__any_sync(0xffffffffu, move)) {
-          const float m_new = move ? mx[0] * kC2 : m_ref;
+          const float m_new = move ? fminf(mx[0] * kC2, INFINITY) : m_ref;  // (fminf drops a NaN)
           if (j > 0) {
             // (P V of tile j - 3 was done before these scores: the parity is the last one's)
             ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1));
@@ -452,6 +461,7 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     if (ok) {
       tc_fence_after();
       const bool live = t < len;
+      if (!(fabsf(m_ref) < -kLowest)) l = __int_as_float(0x7fffffff);
       const float inv = live ? 1.0f / l : 0.f;
 #pragma unroll
       for (int c0 = 0; c0 < kHd; c0 += 32)  // over Q, which nothing reads any more

@@ -80,3 +80,59 @@ def test_attention_key_at_minus_infinity(T, dtype):
         t3, do = _one_head(dtype, T, 4)
         t3[:, 0, 3], t3[at, 1, 3] = 1.0, -math.inf
         _check_pattern(t3, do)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("T", [1, 2, 20, 64, 70, 140])
+def test_attention_shows_values_that_are_not_finite(T, which, value, dtype):
+    """One channel of one live row of q, k or v, at every index modulo 8 and in every tile."""
+    for at in sorted({j for j in (*range(8), 63, 64, 65, 127, 128, T - 1) if j < T}):
+        t3, do = _one_head(dtype, T, 5)
+        t3[at, which, 9] = value
+        _check_pattern(t3, do)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_attention_shows_them_beside_padded_rows(value, dtype):
+    for frames, at in ((1, 0), (2, 1), (66, 64), (66, 3), (130, 129)):
+        t3, do = _one_head(dtype, 150, 6)
+        t3[frames:], do[frames:] = math.nan, math.nan
+        t3[at, 1, 0] = value
+        _check_pattern(t3, do, frames)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T", [1, 2, 9, 100])
+def test_attention_rows_without_a_score(T, dtype):
+    """Every score of a row is -infinity: no softmax."""
+    t3, do = _one_head(dtype, T, 7)
+    t3[0, 0, 3] = -math.inf
+    t3[:, 1, 3] = 1.0
+    _check_pattern(t3, do)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_scores_of_minus_infinity_before_others(dtype):
+    """The first tile's scores are all -infinity, the second's are not: the row has the second's softmax."""
+    t3, do = _one_head(dtype, 100, 8)
+    t3[:, 0, 3] = 1.0
+    t3[:70, 1, 3] = -math.inf
+    _check_pattern(t3, do)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("at", range(8))
+def test_attention_overflowed_scores(at, sign):
+    """A product of finite rows that passes fp32's range: +infinity, which shows, or -infinity, a weight of zero."""
+    t3, do = _one_head(BF16, 40, 9)
+    t3[:, :2, 2] = 0.0
+    t3[1, 0, 2], t3[at, 1, 2] = 1e30, sign * 1e10
+    got, lse = _kernels(t3, do)
+    bad = torch.zeros(40, dtype=torch.bool)
+    bad[1] = sign > 0
+    assert torch.equal(torch.isnan(lse), bad)
+    for name, rows in (("out", bad), ("dq", bad), ("dk", bad.any().expand(40)), ("dv", bad.any().expand(40))):
+        assert torch.equal(~torch.isfinite(got[name]), rows[:, None].expand(40, 64)), name
