@@ -408,7 +408,10 @@ def _workspace(ws, nbytes: int, device, stream):
     if stream is None:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     else:
-        with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=device)):
+        handle = _stream(stream)
+        # (0 is the default stream; ExternalStream takes it for none given and makes another one)
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device) if handle
+                               else torch.cuda.default_stream(device)):
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return ws.data_ptr(), nbytes, ws
 

@@ -136,3 +136,58 @@ def test_attention_overflowed_scores(at, sign):
     assert torch.equal(torch.isnan(lse), bad)
     for name, rows in (("out", bad), ("dq", bad), ("dk", bad.any().expand(40)), ("dv", bad.any().expand(40))):
         assert torch.equal(~torch.isfinite(got[name]), rows[:, None].expand(40, 64)), name
+
+
+# --------------------------------------------------------- streams given by handle
+
+
+def _owner(address):
+    """The stream whose pool holds an address of torch's allocator."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= address < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not an address of the allocator")
+
+
+def test_workspaces_belong_to_the_default_stream_when_it_is_named():
+    dev = torch.device("cuda", torch.cuda.current_device())
+    side = torch.cuda.Stream()
+    for stream, handle in ((None, 0), (0, 0), (torch.cuda.default_stream(), 0), (side, side.cuda_stream),
+                           (side.cuda_stream, side.cuda_stream)):
+        pointer, _, owner = B._workspace(None, 1 << 12, dev, stream)
+        assert pointer == owner.data_ptr() and _owner(pointer) == handle
+    with torch.cuda.stream(side):  # the default stream by name, from another one
+        pointer, _, owner = B._workspace(None, 1 << 12, dev, 0)
+        assert _owner(pointer) == 0
+
+
+@pytest.mark.parametrize("by", ["handle", "object"])
+def test_calls_on_the_default_stream_by_name(by):
+    """With other streams allocating and writing meanwhile, the results are those of the same calls unnamed."""
+    stream = 0 if by == "handle" else torch.cuda.default_stream()
+    gen = torch.Generator().manual_seed(12)
+    q, k, v, do = (torch.randn(2, 500, 256, generator=gen).half().cuda() for _ in range(4))
+    x, gamma = torch.randn(6000, 512, generator=gen).cuda(), torch.ones(512, device="cuda")
+    err, sides = _err(), [torch.cuda.Stream() for _ in range(8)]
+
+    def calls(s):
+        out, lse = torch.empty_like(q), torch.empty(2, 4, 500, device="cuda")
+        grads = [torch.empty_like(q) for _ in range(3)]
+        dx, mean, rstd = torch.empty_like(x), torch.zeros(6000, device="cuda"), torch.ones(6000, device="cuda")
+        dg, db, norm = (torch.empty(n, device="cuda") for n in (512, 512, 1))
+        B.w2v_op_attention_fwd(q, k, v, out, lse, err, stream=s)
+        B.w2v_op_attention_bwd(do, q, k, v, out, lse, *grads, err, stream=s)
+        B.w2v_op_layernorm_bwd(x, x, gamma, gamma, mean, rstd, 0, None, dx, dg, db, stream=s)
+        B.w2v_op_grad_clip([dx], [dx], 1.0, 1.0, norm, stream=s)
+        return (*grads, dx, dg, db, norm)
+
+    alone = calls(None)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = calls(stream)
+        for s in sides:
+            with torch.cuda.stream(s):
+                torch.full((1 << 18,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert all(torch.equal(a, b) for a, b in zip(alone, got))
