@@ -9,8 +9,13 @@
  * to the next, so each may be recorded into a CUDA graph.  Scratch is a
  * workspace that the caller passes (16-byte aligned device memory of at least
  * the size its w2v_op_*_workspace function returns; nothing in it needs to be
- * initialised or kept; a size of 0 means that NULL will do).  Calls whose work may overlap on the GPU — two
- * streams, two graphs — need a workspace each.
+ * initialised or kept; a size of 0 means that NULL will do).  Calls whose work
+ * may overlap on the GPU — two streams, two graphs — need a workspace each.
+ *
+ * What a call writes (outputs, workspace, error word) must not share memory with
+ * anything else that it reads or writes, except where a call says so; rows that lie
+ * between one another's, as those of a fused projection, do not.  A call whose
+ * operands do is refused with W2V_EINVAL.
  *
  * Sums run in a fixed order: the same call gives the same bits.
  */
@@ -53,8 +58,8 @@ typedef struct {
  * none above -infinity, has no softmax: its out and lse are NaN.
  * Scores, softmax and sums are fp32; the probabilities are rounded to dtype for
  * the product with v.
- * Errors: W2V_EINVAL (null or misaligned pointer, dtype, strides), W2V_ESHAPE
- * (batch, T or H < 1, T or the number of tiles too large), W2V_ECUDA. */
+ * Errors: W2V_EINVAL (null or misaligned pointer, dtype, strides, overlap),
+ * W2V_ESHAPE (batch, T or H < 1, T or the number of tiles too large), W2V_ECUDA. */
 int w2v_op_attention_fwd(const w2v_attention_shape* shape, const void* q, const void* k, const void* v, void* out,
                          float* lse, int* err_dev, void* stream);
 
@@ -73,7 +78,7 @@ size_t w2v_op_attention_bwd_workspace(int batch, int T, int H);
  * P and dS are rounded to dtype for the products (dS, in fp16, after scaling by
  * a power of two per clip and head that keeps it in range); everything else is
  * fp32.  No atomics.  Errors as above, and W2V_EINVAL if ws_bytes is too
- * small.  The outputs must not overlap the inputs or one another. */
+ * small. */
 int w2v_op_attention_bwd(const w2v_attention_shape* shape, const void* dout, const void* q, const void* k,
                          const void* v, const void* out, const float* lse, void* dq, void* dk, void* dv, void* ws,
                          size_t ws_bytes, int* err_dev, void* stream);
@@ -87,10 +92,10 @@ int w2v_op_attention_bwd(const w2v_attention_shape* shape, const void* dout, con
  * are equal, or x is fp32 and y fp16 or bf16 (the fp32 residual stream
  * normalised for the next projection).  x_ld and y_ld: elements between rows,
  * >= cols; any alignment of the element type (rows of 16-byte multiples on
- * 16-byte boundaries are the fast case).  gamma, beta: fp32 [cols].  y must not
- * overlap x.  rows = 0 does nothing (x, y, mean and rstd may then be NULL).
- * Errors: W2V_EINVAL (null or misaligned pointer, types, strides, act, eps <= 0),
- * W2V_ESHAPE (rows < 0 or >= 2^31, cols outside [1, W2V_LAYERNORM_MAX_COLS]),
+ * 16-byte boundaries are the fast case).  gamma, beta: fp32 [cols].
+ * rows = 0 does nothing (x, y, mean and rstd may then be NULL).
+ * Errors: W2V_EINVAL (null or misaligned pointer, types, strides, act, eps <= 0,
+ * overlap), W2V_ESHAPE (rows < 0 or >= 2^31, cols outside [1, W2V_LAYERNORM_MAX_COLS]),
  * W2V_ECUDA. */
 int w2v_op_layernorm_fwd(const void* x, int x_type, int64_t x_ld, void* y, int y_type, int64_t y_ld, int64_t rows,
                          int cols, const float* gamma, const float* beta, float eps, int act, float* mean, float* rstd,
@@ -107,7 +112,7 @@ size_t w2v_op_layernorm_bwd_workspace(int64_t rows, int cols);
  *   dgamma = sum_rows dz xh,  dbeta = sum_rows dz     (fp32 [cols], overwritten).
  * dy is of y_type; dres (the gradient that reached x past the LayerNorm, or NULL
  * for none) and dx are of x_type.  dx may be dres, with the same stride (the sum
- * in place); otherwise no output may overlap an input.
+ * in place).
  * rows = 0 writes zeros to dgamma and dbeta.  Errors as above, and W2V_EINVAL if
  * ws_bytes is too small. */
 int w2v_op_layernorm_bwd(const void* dy, int y_type, int64_t dy_ld, const void* x, int x_type, int64_t x_ld,

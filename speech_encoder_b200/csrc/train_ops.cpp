@@ -8,6 +8,7 @@
 #include <new>
 #include <vector>
 
+#include "extent.h"
 #include "w2v.h"
 #include "w2v_internal.h"
 
@@ -77,12 +78,31 @@ int layernorm_args(int x_type, int64_t x_ld, int y_type, int64_t y_ld, int64_t r
 
 size_t type_size(int t) { return t == W2V_F32 ? 4 : 2; }
 
+constexpr int64_t kMostStride = int64_t(1) << 56;  // elements: longer rows than any memory holds
+
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // A workspace of no bytes may be anything.
 bool workspace_ok(const void* ws, size_t has, size_t needs) {
   return needs == 0 || (ws && aligned16(ws) && has >= needs);
 }
+
+// The operands of a call: false if one that is written shares memory with another
+// one, or if one is longer than any memory.
+struct Operands {
+  Extent writes[5], reads[7];
+  int n_writes = 0, n_reads = 0;
+  bool fit = true;
+  void rows(bool write, const void* p, int64_t width, int64_t stride0, int64_t n0, int64_t stride1 = 0, int64_t n1 = 1) {
+    fit = make_extent(p, width, stride0, n0, stride1, n1, write ? writes + n_writes++ : reads + n_reads++) && fit;
+  }
+  void bytes(bool write, const void* p, int64_t n) { rows(write, p, n, 0, 1); }
+  // one 16-bit operand of an attention call; strides in elements
+  void clips(bool write, const void* p, const AttnTrain& a, int64_t ld, int64_t bs) {
+    rows(write, p, 128 * static_cast<int64_t>(a.H), 2 * ld, a.T, a.batch == 1 ? 0 : 2 * bs, a.batch);
+  }
+  bool apart() const { return fit && !writes_overlap(writes, n_writes, reads, n_reads); }
+};
 
 }  // namespace
 
@@ -95,6 +115,13 @@ extern "C" int w2v_op_attention_fwd(const w2v_attention_shape* shape, const void
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned_to(lse, 4) ||
       !aligned_to(err_dev, 4))
     return W2V_EINVAL;
+  Operands o;
+  for (const void* p : {q, k, v}) o.clips(false, p, a, a.qkv_ld, a.qkv_bs);
+  if (a.frames) o.bytes(false, a.frames, 4 * static_cast<int64_t>(a.batch));
+  o.clips(true, out, a, a.out_ld, a.out_bs);
+  o.bytes(true, lse, 4 * static_cast<int64_t>(a.batch) * a.H * a.T);
+  o.bytes(true, err_dev, 4);
+  if (!o.apart()) return W2V_EINVAL;
   return status(launch_attention_fwd(a, q, k, v, out, lse, err_dev, static_cast<cudaStream_t>(stream)));
 }
 
@@ -114,7 +141,17 @@ extern "C" int w2v_op_attention_bwd(const w2v_attention_shape* shape, const void
                         static_cast<const void*>(dv)})
     if (!aligned16(p)) return W2V_EINVAL;
   if (!aligned_to(lse, 4) || !aligned_to(err_dev, 4)) return W2V_EINVAL;
-  if (!workspace_ok(ws, ws_bytes, attention_bwd_ws_bytes(a.batch, a.T, a.H))) return W2V_EINVAL;
+  const size_t needs = attention_bwd_ws_bytes(a.batch, a.T, a.H);
+  if (!workspace_ok(ws, ws_bytes, needs)) return W2V_EINVAL;
+  Operands o;
+  for (const void* p : {q, k, v}) o.clips(false, p, a, a.qkv_ld, a.qkv_bs);
+  for (const void* p : {out, dout}) o.clips(false, p, a, a.out_ld, a.out_bs);
+  o.bytes(false, lse, 4 * static_cast<int64_t>(a.batch) * a.H * a.T);
+  if (a.frames) o.bytes(false, a.frames, 4 * static_cast<int64_t>(a.batch));
+  for (const void* p : {dq, dk, dv}) o.clips(true, p, a, a.grad_ld, a.grad_bs);
+  o.bytes(true, ws, static_cast<int64_t>(needs));
+  o.bytes(true, err_dev, 4);
+  if (!o.apart()) return W2V_EINVAL;
   return status(launch_attention_bwd(a, dout, q, k, v, out, lse, dq, dk, dv, ws, err_dev,
                                      static_cast<cudaStream_t>(stream)));
 }
@@ -130,6 +167,14 @@ extern "C" int w2v_op_layernorm_fwd(const void* x, int x_type, int64_t x_ld, voi
   if (!aligned_to(x, type_size(x_type)) || !aligned_to(y, type_size(y_type)) || !aligned_to(mean, 4) ||
       !aligned_to(rstd, 4) || !aligned_to(gamma, 4) || !aligned_to(beta, 4))
     return W2V_EINVAL;
+  Operands o;
+  const int64_t xs = type_size(x_type), ys = type_size(y_type);
+  if (x_ld > kMostStride || y_ld > kMostStride) return W2V_EINVAL;
+  o.rows(false, x, xs * cols, xs * x_ld, rows);
+  for (const float* p : {gamma, beta}) o.bytes(false, p, 4 * static_cast<int64_t>(cols));
+  o.rows(true, y, ys * cols, ys * y_ld, rows);
+  for (const float* p : {mean, rstd}) o.bytes(true, p, 4 * rows);
+  if (!o.apart()) return W2V_EINVAL;
   return status(launch_layernorm_fwd(a, x, y, eps, mean, rstd, static_cast<cudaStream_t>(stream)));
 }
 
@@ -152,7 +197,21 @@ extern "C" int w2v_op_layernorm_bwd(const void* dy, int y_type, int64_t dy_ld, c
       !aligned_to(dres, type_size(x_type)) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(gamma, 4) ||
       !aligned_to(beta, 4) || !aligned_to(dgamma, 4) || !aligned_to(dbeta, 4))
     return W2V_EINVAL;
-  if (!workspace_ok(ws, ws_bytes, layernorm_bwd_ws_bytes(rows, cols))) return W2V_EINVAL;
+  const size_t needs = layernorm_bwd_ws_bytes(rows, cols);
+  if (!workspace_ok(ws, ws_bytes, needs)) return W2V_EINVAL;
+  Operands o;
+  const int64_t xs = type_size(x_type), ys = type_size(y_type);
+  if (x_ld > kMostStride || dy_ld > kMostStride || dx_ld > kMostStride || (dres && dres_ld > kMostStride))
+    return W2V_EINVAL;
+  o.rows(false, dy, ys * cols, ys * dy_ld, rows);
+  o.rows(false, x, xs * cols, xs * x_ld, rows);
+  if (dres && dres != dx) o.rows(false, dres, xs * cols, xs * dres_ld, rows);
+  for (const float* p : {gamma, beta}) o.bytes(false, p, 4 * static_cast<int64_t>(cols));
+  for (const float* p : {mean, rstd}) o.bytes(false, p, 4 * rows);
+  o.rows(true, dx, xs * cols, xs * dx_ld, rows);
+  for (const float* p : {dgamma, dbeta}) o.bytes(true, p, 4 * static_cast<int64_t>(cols));
+  o.bytes(true, ws, static_cast<int64_t>(needs));
+  if (!o.apart()) return W2V_EINVAL;
   return status(launch_layernorm_bwd(a, dy, x, mean, rstd, dres, dres_ld, dx, dx_ld, dgamma, dbeta, ws,
                                      static_cast<cudaStream_t>(stream)));
 }
@@ -168,14 +227,17 @@ extern "C" int w2v_op_grad_clip(int n, const void* const* grads, void* const* ou
   if (!(scale > 0.f) || !(scale < INFINITY) || !(max_norm > 0.f)) return W2V_EINVAL;
   if (!workspace_ok(ws, ws_bytes, grad_clip_ws_bytes(n))) return W2V_EINVAL;
   try {
-    // Byte ranges written, and each tensor's read range: an output may be its own
-    // gradient's memory, and nothing else that the call reads or writes.
+    // Byte ranges written (the norm and the workspace among them), and each tensor's
+    // read range: an output may be its own gradient's memory, and nothing else that the
+    // call reads or writes.
     struct Range {
       uintptr_t from, to;
-      int tensor;
     };
     std::vector<Range> ranges;
-    ranges.reserve(2 * static_cast<size_t>(n));
+    ranges.reserve(2 * static_cast<size_t>(n) + 2);
+    const uintptr_t norm_at = reinterpret_cast<uintptr_t>(norm_dev), ws_at = reinterpret_cast<uintptr_t>(ws);
+    ranges.push_back({norm_at, norm_at + sizeof(float)});
+    ranges.push_back({ws_at, ws_at + grad_clip_ws_bytes(n)});
     for (int i = 0; i < n; ++i) {
       if (!type_ok(types[i])) return W2V_EINVAL;
       if (counts[i] < 0 || counts[i] >= (int64_t(1) << 33)) return W2V_ESHAPE;
@@ -184,8 +246,8 @@ extern "C" int w2v_op_grad_clip(int n, const void* const* grads, void* const* ou
       if (!grads[i] || !outs[i] || !aligned_to(grads[i], size) || !aligned_to(outs[i], size)) return W2V_EINVAL;
       const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(outs[i]);
       const uintptr_t bytes = static_cast<uintptr_t>(counts[i]) * size;
-      ranges.push_back({g, g + bytes, i});
-      if (o != g) ranges.push_back({o, o + bytes, i});
+      ranges.push_back({g, g + bytes});
+      if (o != g) ranges.push_back({o, o + bytes});
     }
     std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
     for (size_t i = 1; i < ranges.size(); ++i)

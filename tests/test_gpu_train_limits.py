@@ -191,3 +191,48 @@ def test_calls_on_the_default_stream_by_name(by):
     torch.cuda.synchronize()
     assert int(err.item()) == 0
     assert all(torch.equal(a, b) for a, b in zip(alone, got))
+
+
+# ------------------------------------------------------ memory shared row by row
+
+
+def test_layernorm_operands_between_one_another():
+    """fp32 rows, their fp16 rows and the gradients side by side in the rows of one buffer: apart, though their
+    ranges are not."""
+    gen = torch.Generator().manual_seed(14)
+    rows, cols = 90, 256
+    wide = torch.zeros(rows, 4 * cols, device="cuda")
+    x, dx, dres, half = (wide[:, i * cols:(i + 1) * cols] for i in range(4))
+    half = half.view(F16)
+    y, dy = half[:, :cols], half[:, cols:]
+    x.copy_(torch.randn(rows, cols, generator=gen))
+    dres.copy_(torch.randn(rows, cols, generator=gen))
+    dy.copy_(torch.randn(rows, cols, generator=gen))
+    gamma, beta = torch.randn(2, cols, generator=gen).cuda()
+    stats = torch.empty(2, rows, device="cuda")
+    sums = torch.empty(4, cols, device="cuda")
+    B.w2v_op_layernorm_fwd(x, y, gamma, beta, 1e-5, 1, *stats)
+    B.w2v_op_layernorm_bwd(dy, x, gamma, beta, *stats, 1, dres, dx, sums[0], sums[1])
+    y2, dx2 = torch.empty(rows, cols, dtype=F16, device="cuda"), torch.empty(rows, cols, device="cuda")
+    stats2 = torch.empty(2, rows, device="cuda")
+    B.w2v_op_layernorm_fwd(x.contiguous(), y2, gamma, beta, 1e-5, 1, *stats2)
+    B.w2v_op_layernorm_bwd(dy.contiguous(), x.contiguous(), gamma, beta, *stats2, 1, dres.contiguous(), dx2, sums[2],
+                           sums[3])
+    assert torch.equal(y, y2) and torch.equal(dx, dx2) and torch.equal(stats, stats2) and torch.equal(sums[:2], sums[2:])
+    with pytest.raises(B.W2VError):
+        B.w2v_op_layernorm_bwd(dy, x, gamma, beta, *stats, 1, dres, x, sums[0], sums[1])
+    with pytest.raises(B.W2VError):
+        B.w2v_op_layernorm_fwd(x, wide[:, 1:cols + 1], gamma, beta, 1e-5, 0, *stats)
+
+
+def test_attention_gradients_over_their_operands_are_refused():
+    q, k, v, do = torch.randn(4, 2, 70, 128, device="cuda").half()
+    out, lse, err = torch.empty_like(q), torch.empty(2, 2, 70, device="cuda"), _err()
+    B.w2v_op_attention_fwd(q, k, v, out, lse, err)
+    dq, dk, dv = torch.empty(3, 2, 70, 128, dtype=F16, device="cuda")
+    B.w2v_op_attention_bwd(do, q, k, v, out, lse, dq, dk, dv, err)
+    for bad in ((q, dk, dv), (dq, k, dv), (dq, dk, do), (dq, dq, dv), (out, dk, dv)):
+        with pytest.raises(B.W2VError):
+            B.w2v_op_attention_bwd(do, q, k, v, out, lse, *bad, err)
+    with pytest.raises(B.W2VError):
+        B.w2v_op_attention_fwd(q, k, v, v, lse, err)
