@@ -8,7 +8,7 @@
 // fp32 throughout; only y and dx are rounded to their types.  Each row is read
 // once and used from registers; without a GELU the passes come within 1.2 to 1.5 of
 // the time that HBM needs, with one instruction issue bounds them (51199 x 512 fp16:
-// forward 19 us and 24 with the exact GELU against 16, backward 35 and 46 against 24).
+// forward 20 us and 25 with the exact GELU against 16, backward 36 and 47 against 24).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -149,28 +149,62 @@ __device__ __forceinline__ float2 held(float v) {
 }
 
 // GELU f and its slope f' on pairs of elements in packed fp32 instructions (with
-// scalar ones both passes over 51199 x 512 were bound by instruction issue).
-template <int ACT>
+// scalar ones both passes over 51199 x 512 were bound by instruction issue).  WIDE:
+// for results that stay fp32.
+template <int ACT, bool WIDE>
 struct Gelu {
   __device__ __forceinline__ float2 value(float2 z) const { return z; }
   __device__ __forceinline__ float2 slope(float2) const { return both(1.0f); }
 };
 
-// Exact form.  h = Phi(-|z|) and e = exp(-z^2 / 2) share one exponential: erfc by
-// formula 7.1.26 of Abramowitz and Stegun's Handbook (Hastings), a polynomial in
-// 1 / (1 + p x) times e, absolute error below 0.75e-7 in Phi.
+// Phi(-|z|) of the exact form, and e = exp(-z^2 / 2): they share one exponential, as
+// Phi(-|z|) = e g(t) with t = 1 / (1 + p |z|) and g a polynomial without a constant.
+// Coefficients by linear programming over a grid of z in [0, 13] or [0, 14], p by search.
+template <bool WIDE>
+struct NormalTail;
+
+// Results of 16 bits: degree 6, the smallest largest excess over absolute and relative
+// bounds of 1 : 1000 (6.4e-8 and 6.4e-5).  Measured over [-13, 13]: the slope within
+// 2.5e-7, and f, rounded, within 1.16 half steps of fp16 and 1.03 of bf16 (a polynomial
+// for the absolute error alone was up to 2.9 and, at -8, 18 off).
 template <>
-struct Gelu<1> {
+struct NormalTail<false> {
+  static constexpr float p = 0.2925f;
   float2 a = held(-0.5f * 1.4426950408889634f);
-  float2 c5 = held(0.5f * 1.061405429f), c4 = held(0.5f * -1.453152027f), c3 = held(0.5f * 1.421413741f);
-  float2 c2 = held(0.5f * -0.284496736f), c1 = held(0.5f * 0.254829592f);
+  float2 c6 = held(-0.08600358808141047f), c5 = held(0.26645464523659707f), c4 = held(-0.07094969882740387f);
+  float2 c3 = held(0.16799627886898685f), c2 = held(0.10494842715972288f), c1 = held(0.11755387193946223f);
+  __device__ __forceinline__ float2 g(float2 t) const {
+    return ffma2(ffma2(ffma2(ffma2(ffma2(t, c6, c5), t, c4), t, c3), t, c2), t, c1);
+  }
+};
+
+// Results of fp32: degree 8, the smallest largest relative error (6.6e-8), so a few
+// roundings of fp32 at every z, and z^2 2^-23 of the exponent's.  Measured: Phi within
+// 2.2e-7, f within 1.5e-6 of its own value down to z = -5, the slope within 2.3e-7.
+// Packed like the other; fp32 rows wait for memory and hardly show it (25600 x 512
+// forward 18.7 us for either degree, backward 33.2 for 33.0).
+template <>
+struct NormalTail<true> {
+  static constexpr float p = 0.305f;
+  float2 a = held(-0.5f * 1.4426950408889634f);
+  float2 c8 = held(0.03663970305112069f), c7 = held(-0.15273976910813133f), c6 = held(0.1853005931000754f);
+  float2 c5 = held(-0.03761743553585788f), c4 = held(0.12085047515807737f), c3 = held(0.10346547345964746f);
+  float2 c2 = held(0.12246101027285013f), c1 = held(0.12164002060621362f);
+  __device__ __forceinline__ float2 g(float2 t) const {
+    const float2 high = ffma2(ffma2(ffma2(ffma2(t, c8, c7), t, c6), t, c5), t, c4);
+    return ffma2(ffma2(ffma2(high, t, c3), t, c2), t, c1);
+  }
+};
+
+// Exact form; h = Phi(-|z|).
+template <bool WIDE>
+struct Gelu<1, WIDE> : NormalTail<WIDE> {
   __device__ __forceinline__ float2 tail(float2 z, float2* e) const {
-    constexpr float p = 0.3275911f * 0.70710678118654752f;
+    constexpr float p = NormalTail<WIDE>::p;
     const float2 t = make_float2(rcp_approx(fmaf(fabsf(z.x), p, 1.0f)), rcp_approx(fmaf(fabsf(z.y), p, 1.0f)));
-    const float2 w = fmul2(fmul2(z, a), z);
+    const float2 w = fmul2(fmul2(z, this->a), z);
     *e = make_float2(ex2_approx(w.x), ex2_approx(w.y));
-    const float2 te = fmul2(t, *e);
-    return fmul2(ffma2(ffma2(ffma2(ffma2(t, c5, c4), t, c3), t, c2), t, c1), te);
+    return fmul2(this->g(t), fmul2(t, *e));
   }
   // z Phi(z) = max(z, 0) - |z| Phi(-|z|)
   __device__ __forceinline__ float2 value(float2 z) const {
@@ -189,8 +223,8 @@ struct Gelu<1> {
 };
 
 // Tanh form: z s with s = sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3).
-template <>
-struct Gelu<2> {
+template <bool WIDE>
+struct Gelu<2, WIDE> {
   static constexpr float k = 0.7978845608028654f, kl = -2.0f * k * 1.4426950408889634f;
   float2 one = held(1.0f), k1 = held(kl), k3 = held(0.044715f * kl);
   __device__ __forceinline__ float2 gate(float2 z, float2 z2) const {
@@ -243,9 +277,15 @@ __host__ __device__ constexpr int chunk_step() {
 
 // G threads a row, each with NCH chunks of V elements; a group takes ROWS rows at
 // once (two where there are rows enough: a warp with one 1 KB row in flight reaches
-// 4.4 TB/s of the 6.5).
+// 4.4 TB/s of the 6.5).  Blocks an SM, where the compiler's own choice of registers is
+// the worse one: two rows fit four blocks (with three 51199 x 512 fp16 takes 22 us for
+// 20), and fp32 rows of 513 to 768 columns are faster with the registers of three, gamma
+// and beta on their way early (7992 x 768 fp32 10.0 us for 10.8; 0 leaves it the choice).
+template <typename X, int V, int NCH, int G, int ROWS>
+constexpr int kFwdBlocks = ROWS == 2 ? 4 : sizeof(X) == 4 && V == 4 && NCH == 6 && G == 32 ? 3 : 0;
+
 template <typename X, typename Y, int V, int NCH, int G, int ROWS>
-__global__ void __launch_bounds__(kLnThreads)
+__global__ void __launch_bounds__(kLnThreads, kFwdBlocks<X, V, NCH, G, ROWS>)
 layernorm_fwd_kernel(const X* __restrict__ x, int64_t x_ld, Y* __restrict__ y, int64_t y_ld, int64_t rows, int cols,
                      const float* __restrict__ gamma, const float* __restrict__ beta, float eps, int act,
                      float* __restrict__ mean_out, float* __restrict__ rstd_out) {
@@ -303,7 +343,7 @@ layernorm_fwd_kernel(const X* __restrict__ x, int64_t x_ld, Y* __restrict__ y, i
     }
   }
   by_act(act, [&](auto a) {
-    const Gelu<decltype(a)::value> gelu;
+    const Gelu<decltype(a)::value, sizeof(Y) == 4> gelu;
 #pragma unroll
     for (int e = 0; e < 2 * NP; e += 4) {
       const float4 g = load4<V, G>(gamma, lane, cols, e), b = load4<V, G>(beta, lane, cols, e);
@@ -410,7 +450,7 @@ layernorm_bwd_kernel(const Y* __restrict__ dy, int64_t dy_ld, const X* __restric
     // (columns past the end: dy is 0, so they add nothing)
     by_act(act, [&](auto a) {
       constexpr int ACT = decltype(a)::value;
-      const Gelu<ACT> gelu;
+      const Gelu<ACT, sizeof(X) == 4> gelu;  // (dx is X)
 #pragma unroll
       for (int e = 0; e < 2 * NP; e += 4) {
         const float4 g4 = load4<V, G>(gamma, lane, cols, e);

@@ -236,3 +236,70 @@ def test_attention_gradients_over_their_operands_are_refused():
             B.w2v_op_attention_bwd(do, q, k, v, out, lse, *bad, err)
     with pytest.raises(B.W2VError):
         B.w2v_op_attention_fwd(q, k, v, v, lse, err)
+
+
+# ------------------------------------------------------- GELU over its whole range
+
+
+def _through_layernorm(z, xt, yt, act):
+    """(f(z), f'(z)): one row with gamma 0, beta z and dy 1 has y = f(z) and dbeta = f'(z)."""
+    n = len(z)
+    x = torch.linspace(-1, 1, n, device="cuda").to(xt)[None]
+    zero, y, dx = torch.zeros(n, device="cuda"), torch.empty(1, n, dtype=yt, device="cuda"), torch.empty_like(x)
+    mean, rstd, dgamma, dbeta = (torch.empty(k, device="cuda") for k in (1, 1, n, n))
+    B.w2v_op_layernorm_fwd(x, y, zero, z, 1e-5, act, mean, rstd)
+    B.w2v_op_layernorm_bwd(torch.ones_like(y), x, zero, z, mean, rstd, act, None, dx, dgamma, dbeta)
+    return y[0].double().cpu(), dbeta.double().cpu()
+
+
+@pytest.mark.parametrize("xt,yt", [(F32, F32), (F32, F16), (F32, BF16), (F16, F16), (BF16, BF16)])
+@pytest.mark.parametrize("n", [1024, 8192, 1021, 5003])
+def test_exact_gelu_over_its_range(n, xt, yt):
+    """Phi(-|z|) = e g(t), e = exp(-z^2 / 2), t = 1 / (1 + p |z|), counted in u = 2^-24 of its value: t is off by 3 u
+    (a rounding, and a unit of the approximate reciprocal), which g takes up to 2.6 times; e by 2.8 u (the approximate
+    exponential's 2^-22.5) and 1.5 z^2 u of its argument's roundings; the polynomial by 12 u of its coefficients' and
+    steps' roundings (the magnitudes of its terms are at most 1.8 times their sum) and 1.1 u of its own error; two
+    products.  Together 28 u + 1.5 z^2 u, held to 2^-19 + z^2 2^-23.  With 16-bit results the polynomial's own error is
+    up to 6.4e-5 of Phi(-|z|) and 6.4e-8; the value is then rounded to its type."""
+    u = 2.0 ** -24
+    for part in range(4):
+        z = torch.linspace(-13, 13, 4 * n)[part::4].contiguous().cuda()
+        y, slope = _through_layernorm(z, xt, yt, 1)
+        zd = z.double().cpu()
+        tail = torch.special.erfc(zd.abs() / math.sqrt(2)) / 2
+        phi = torch.exp(-zd * zd / 2) / math.sqrt(2 * math.pi)
+        relative = 2.0 ** -19 + zd * zd * 2.0 ** -23
+
+        def off(wide):  # of Phi(-|z|)
+            return tail * relative + (0 if wide else torch.minimum(6.5e-5 * tail, torch.tensor(6.5e-8)))
+
+        cdf = torch.where(zd < 0, tail, 1 - tail)
+        want = zd * cdf
+        half = torch.finfo(yt).eps / 2
+        limit = (half + u) * want.abs() + zd.abs() * off(yt == F32) * (1 + half) + R.tiny(yt)
+        assert ((y - want).abs() <= limit).all(), float(((y - want).abs() / limit).max())
+        # Phi(z) + z phi(z): two roundings of at most 1.13, and z phi with the error of e
+        limit = off(xt == F32) + zd.abs() * phi * relative + 2 * 1.13 * u
+        err = (slope - (cdf + zd * phi)).abs()
+        assert (err <= limit).all(), float((err / limit).max())
+
+
+@pytest.mark.parametrize("xt,yt", [(F32, F32), (F16, F16)])
+def test_tanh_gelu_over_its_range(xt, yt):
+    """s = sigmoid(2 u(z)) with an exponent up to 2 u(13) = 172: off by 4 of its roundings and those of the approximate
+    instructions, in proportion to the smaller of s and 1 - s and otherwise 2 u of s.  Below 2^-126 s counts as zero."""
+    u, n = 2.0 ** -24, 4099
+    z = torch.linspace(-13, 13, n).cuda()
+    y, slope = _through_layernorm(z, xt, yt, 2)
+    zd = z.double().cpu()
+    w = 2 * math.sqrt(2 / math.pi) * (zd + 0.044715 * zd ** 3)
+    s, dw = torch.sigmoid(w), 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * zd * zd)
+    off = s * ((4 * w.abs() + 4) * torch.sigmoid(-w) + 4) * u
+    half = torch.finfo(yt).eps / 2
+    want = zd * s
+    limit = (half + 2 * u) * want.abs() + zd.abs() * (off + 2.0 ** -126) * (1 + half) + R.tiny(yt)
+    assert ((y - want).abs() <= limit).all(), float(((y - want).abs() / limit).max())
+    # s + z s (1 - s) dw: the product z s - z s s loses what it cancels, a rounding of z s times dw
+    limit = (off + 2.0 ** -126) * (1 + 2 * zd.abs() * dw) + 4 * u * (s + zd.abs() * s * dw)
+    err = (slope - (s + zd * s * (1 - s) * dw)).abs()
+    assert (err <= limit).all(), float((err / limit).max())
