@@ -303,3 +303,27 @@ def test_tanh_gelu_over_its_range(xt, yt):
     limit = (off + 2.0 ** -126) * (1 + 2 * zd.abs() * dw) + 4 * u * (s + zd.abs() * s * dw)
     err = (slope - (s + zd * s * (1 - s) * dw)).abs()
     assert (err <= limit).all(), float((err / limit).max())
+
+
+# -------------------------------------------------- sums that one row more decides
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("xt,yt", [(F16, F16), (BF16, BF16), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("rows,cols", [(1, 256), (63, 512), (64, 1024), (65, 256), (9, 2048), (300, 2048), (1184, 1024),
+                                       (1185, 768), (2367, 512), (2369, 512), (7105, 256), (20011, 256), (4737, 255),
+                                       (301, 1027)])
+def test_layernorm_affine_gradients_count_every_row_once(rows, cols, xt, yt, residual):
+    """Small whole numbers with mean 0 and rstd 1: every partial sum is a whole number below 2^24, so dgamma and dbeta
+    are exact, and a row left out, or taken twice, shows."""
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+    x = torch.randint(-4, 5, (rows, cols), generator=gen, device="cuda")
+    dy = torch.randint(-8, 9, (rows, cols), generator=gen, device="cuda")
+    dy[:, 0], x[:, 0] = 3, 1  # a column that counts them
+    one, zero = torch.ones(cols, device="cuda"), torch.zeros(cols, device="cuda")
+    dgamma, dbeta = torch.full((2, cols), math.nan, device="cuda")
+    xx, res = x.to(xt), torch.zeros(rows, cols, dtype=xt, device="cuda")
+    B.w2v_op_layernorm_bwd(dy.to(yt), xx, one, zero, torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda"), 0,
+                           res if residual else None, torch.empty_like(xx), dgamma, dbeta)
+    assert torch.equal(dgamma.long(), (dy * x).sum(0)) and torch.equal(dbeta.long(), dy.sum(0))
+    assert int(dbeta[0]) == int(dgamma[0]) == 3 * rows
