@@ -327,3 +327,60 @@ def test_layernorm_affine_gradients_count_every_row_once(rows, cols, xt, yt, res
                            res if residual else None, torch.empty_like(xx), dgamma, dbeta)
     assert torch.equal(dgamma.long(), (dy * x).sum(0)) and torch.equal(dbeta.long(), dy.sum(0))
     assert int(dbeta[0]) == int(dgamma[0]) == 3 * rows
+
+
+# --------------------------------------------- short clips, many of them, some empty
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("Bn,T", [(3, 100), (33, 100), (64, 128), (70, 100), (70, 17)])
+def test_attention_many_short_ragged_clips(Bn, T, dtype):
+    """Up to 128 frames one launch makes the statistics, the gradients and the zeros of empty clips; up to 64 clips it
+    takes them by length, more as they come."""
+    gen = torch.Generator().manual_seed(Bn * T)
+    frames = torch.randint(0, T + 1, (Bn,), generator=gen).tolist()
+    frames[0], frames[1], frames[-1] = 0, T, 0
+    t3 = torch.randn(Bn, T, 3, 128, generator=gen).to(dtype)
+    do = (0.1 * torch.randn(Bn, T, 128, generator=gen)).to(dtype)
+    for b, n in enumerate(frames):
+        t3[b, n:], do[b, n:] = math.nan, math.nan
+    q, k, v = (t3.cuda()[:, :, i] for i in range(3))
+    out, lse, err = torch.full((Bn, T, 128), math.nan, dtype=dtype, device="cuda"), torch.empty(Bn, 2, T, device="cuda"), _err()
+    grads = [torch.full_like(out, math.nan) for _ in range(3)]
+    fr = torch.tensor(frames, dtype=torch.int32, device="cuda")
+    B.w2v_op_attention_fwd(q, k, v, out, lse, err, frames=fr)
+    B.w2v_op_attention_bwd(do.cuda(), q, k, v, out, lse, *grads, err, frames=fr)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    want, tol, lse64 = R.attention(t3[:, :, 0], t3[:, :, 1], t3[:, :, 2], 2, frames, do, out.cpu())
+    R.close(out, want["out"], tol["out"], "out")
+    assert torch.equal(lse.cpu() == -math.inf, lse64 == -math.inf)
+    for name, g in zip(("dq", "dk", "dv"), grads):
+        R.close(g, want[name], tol[name], name)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("T", [5, 100, 300])
+def test_attention_of_empty_clips_alone(T, dtype):
+    q = torch.full((3, T, 64), math.nan, dtype=dtype, device="cuda")
+    out, lse, err = q.clone(), torch.zeros(3, 1, T, device="cuda"), _err()
+    grads, fr = [q.clone() for _ in range(3)], torch.tensor([0, -3, 0], dtype=torch.int32, device="cuda")
+    B.w2v_op_attention_fwd(q, q, q, out, lse, err, frames=fr)
+    B.w2v_op_attention_bwd(q, q, q, q, out, lse, *grads, err, frames=fr)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and (lse == -math.inf).all() and all((t == 0).all() for t in (out, *grads))
+
+
+@pytest.mark.parametrize("rows,cols,xt,yt", [(40, 513, F32, F16), (300, 2048, F16, F16), (3000, 255, BF16, BF16),
+                                             (2400, 512, F32, F32)])
+def test_layernorm_residual_in_place_at_other_widths(rows, cols, xt, yt):
+    gen = torch.Generator().manual_seed(cols)
+    x, dres = (torch.randn(rows, cols, generator=gen).to(xt).cuda() for _ in range(2))
+    dy = torch.randn(rows, cols, generator=gen).to(yt).cuda()
+    gamma, beta = torch.randn(2, cols, generator=gen).cuda()
+    mean, rstd, y = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.empty_like(dy)
+    B.w2v_op_layernorm_fwd(x, y, gamma, beta, 1e-5, 2, mean, rstd)
+    dx, sums = torch.empty_like(x), torch.empty(4, cols, device="cuda")
+    B.w2v_op_layernorm_bwd(dy, x, gamma, beta, mean, rstd, 2, dres, dx, sums[0], sums[1])
+    B.w2v_op_layernorm_bwd(dy, x, gamma, beta, mean, rstd, 2, dres, dres, sums[2], sums[3])
+    assert torch.equal(dx, dres) and torch.equal(sums[:2], sums[2:])
