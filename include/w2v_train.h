@@ -77,8 +77,9 @@ size_t w2v_op_attention_bwd_workspace(int batch, int T, int H);
  * frames dk too.
  * P and dS are rounded to dtype for the products (dS, in fp16, after scaling by
  * a power of two per clip and head that keeps it in range); everything else is
- * fp32.  No atomics.  Errors as above, and W2V_EINVAL if ws_bytes is too
- * small. */
+ * fp32.  In fp16 a row whose |rowsum| or 8 |lse| is above 65504 * 2^15 (2^31) has
+ * gradients that are not finite.  No atomics.  Errors as above, and W2V_EINVAL if
+ * ws_bytes is too small. */
 int w2v_op_attention_bwd(const w2v_attention_shape* shape, const void* dout, const void* q, const void* k,
                          const void* v, const void* out, const float* lse, void* dq, void* dk, void* dv, void* ws,
                          size_t ws_bytes, int* err_dev, void* stream);

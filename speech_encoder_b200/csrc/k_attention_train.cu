@@ -490,11 +490,18 @@ attention_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 // in the fp32 accumulator.  Without them every thread of a key CTA read two
 // statistics per column from shared memory (16 wide loads and 16 additions per 32
 // columns, a quarter of its time).  A value is split into three pieces of the
-// operand type, hi + mid + lo, each the rounding of what is left: 24 bits in bf16,
-// 33 in fp16.  fp16's range is widened by groups of three channels with different
-// constants c, of which a value uses the first where value / c fits:
-//   lse:    64 (up to 2^21), 2^15
+// operand type, hi + mid + lo, each the rounding of what is left.  In bf16 that is
+// all of an fp32's 24 bits.  In fp16 it is too until a piece reaches the subnormal
+// step, so the error is absolute: 2^-25 c for a constant c.  fp16's range is widened by
+// groups of three channels with different constants, of which a value uses the first
+// where value / c fits:
+//   8 lse:  64 (up to 2^21), 2^15
 //   rowsum: 2^-24 (up to 2^-10), 2^-14 (1), 2^-4 (2^10), 2^6 (2^20), 2^15
+// From the second group on 2^-25 c is below 2^-28 of the value.  8 lse is off by at
+// most 2^-19 in the first, whatever its size, and a probability by 2^-22 of itself,
+// since lse is added to its exponent; a row sum by 2^-49, less than the smallest
+// product of two fp16 values that dP is a sum of.  Past 65504 * 2^15 a value has no
+// pieces: the row's gradients are not finite.
 // Rows that carry nothing get lse = infinity, so that their probabilities are 0.
 //
 // Layout, per (clip, head): rows padded to a multiple of 128, in the unswizzled
