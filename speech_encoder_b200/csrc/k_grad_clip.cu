@@ -138,14 +138,15 @@ __device__ __forceinline__ double chunk_squares(const void* srcv, int64_t n, int
   return s;
 }
 
+// out = g f lift; lift is 1, or the power of two that keeps f out of fp32's subnormals.
 template <typename T>
-__device__ __forceinline__ void chunk_scale(const void* srcv, void* dstv, int64_t n, int c, float f) {
+__device__ __forceinline__ void chunk_scale(const void* srcv, void* dstv, int64_t n, int c, float f, float lift) {
   constexpr int V = 16 / sizeof(T);
   const T* src = static_cast<const T*>(srcv);
   T* dst = static_cast<T*>(dstv);
   int64_t head, from, to;
   chunk_range<T>(src, n, c, &head, &from, &to);
-  if (c == 0 && threadIdx.x < head) dst[threadIdx.x] = Elem<T>::put(Elem<T>::get(src[threadIdx.x]) * f);
+  if (c == 0 && threadIdx.x < head) dst[threadIdx.x] = Elem<T>::put(Elem<T>::get(src[threadIdx.x]) * f * lift);
   if (to <= from) return;
   const int vecs = static_cast<int>(to - from) / V;
   const bool same = ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) == 0;
@@ -161,7 +162,7 @@ __device__ __forceinline__ void chunk_scale(const void* srcv, void* dstv, int64_
     const int at = threadIdx.x + i * kClipThreads;
     if (at >= vecs) break;
 #pragma unroll
-    for (int k = 0; k < V; ++k) u[i].v[k] = Elem<T>::put(Elem<T>::get(u[i].v[k]) * f);
+    for (int k = 0; k < V; ++k) u[i].v[k] = Elem<T>::put(Elem<T>::get(u[i].v[k]) * f * lift);
     if (same) {
       reinterpret_cast<Vec16<T>*>(dst + from)[at] = u[i];
     } else {
@@ -170,7 +171,7 @@ __device__ __forceinline__ void chunk_scale(const void* srcv, void* dstv, int64_
     }
   }
   const int64_t at = from + static_cast<int64_t>(vecs) * V + threadIdx.x;
-  if (at < to) dst[at] = Elem<T>::put(Elem<T>::get(src[at]) * f);
+  if (at < to) dst[at] = Elem<T>::put(Elem<T>::get(src[at]) * f * lift);
 }
 
 // Sum over the block, the same in every thread, in a fixed order.
@@ -218,19 +219,22 @@ grad_scale_kernel(const __grid_constant__ ClipTable t, const double* __restrict_
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
   double by = static_cast<double>(max_norm) / (norm + 1e-6);
   if (!(by < 1.0) || !(norm < INFINITY)) by = 1.0;  // not clipped, or not a finite norm
-  const float f = static_cast<float>(by * static_cast<double>(scale));
+  by *= static_cast<double>(scale);
+  // A factor below 2^-126 (a norm near fp32's end) would keep but a few bits as an fp32.
+  const float lift = by < 0x1p-126 ? 0x1p-126f : 1.0f;
+  const float f = static_cast<float>(by / static_cast<double>(lift));
   // from the end, where the first pass has just been: what it left in L2 is not
   // read from memory again
   for (int c = t.first[t.count] - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= static_cast<int>(gridDim.x)) {
     const int i = find_tensor(t, c);
     const int k = c - t.first[i];
-    if (f == 1.0f && t.src[i] == t.dst[i]) continue;  // in place and unchanged
+    if (f == 1.0f && lift == 1.0f && t.src[i] == t.dst[i]) continue;  // in place and unchanged
     if (t.type[i] == 2)
-      chunk_scale<float>(t.src[i], t.dst[i], t.n[i], k, f);
+      chunk_scale<float>(t.src[i], t.dst[i], t.n[i], k, f, lift);
     else if (t.type[i] == 1)
-      chunk_scale<__nv_bfloat16>(t.src[i], t.dst[i], t.n[i], k, f);
+      chunk_scale<__nv_bfloat16>(t.src[i], t.dst[i], t.n[i], k, f, lift);
     else
-      chunk_scale<__half>(t.src[i], t.dst[i], t.n[i], k, f);
+      chunk_scale<__half>(t.src[i], t.dst[i], t.n[i], k, f, lift);
   }
 }
 

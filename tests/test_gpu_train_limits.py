@@ -384,3 +384,22 @@ def test_layernorm_residual_in_place_at_other_widths(rows, cols, xt, yt):
     B.w2v_op_layernorm_bwd(dy, x, gamma, beta, mean, rstd, 2, dres, dx, sums[0], sums[1])
     B.w2v_op_layernorm_bwd(dy, x, gamma, beta, mean, rstd, 2, dres, dres, sums[2], sums[3])
     assert torch.equal(dx, dres) and torch.equal(sums[:2], sums[2:])
+
+
+# --------------------------------------------------------------- gradient norm
+
+
+@pytest.mark.parametrize("scale,max_norm", [(2.0 ** -20, 1.0), (1.0, 0.1), (2.0 ** -10, 2.0 ** -30), (2.0 ** -140, math.inf)])
+def test_grad_clip_factors_below_fp32(scale, max_norm):
+    """Large gradients take factors that fp32 holds only as subnormals: the products are as exact as any (three
+    roundings: the factor's, and those of the product)."""
+    gen = torch.Generator().manual_seed(15)
+    g = torch.cat([torch.full((100,), 1e37), 1e37 * torch.randn(900, generator=gen)]).cuda()
+    small = torch.randn(50, generator=gen).cuda()  # ends below fp32's range
+    outs, norm = [torch.empty_like(g), torch.empty_like(small)], torch.empty(1, device="cuda")
+    B.w2v_op_grad_clip([g, small], outs, scale, max_norm, norm)
+    want = scale * math.sqrt(math.fsum(float(t.double().square().sum()) for t in (g, small)))
+    by = min(1.0, max_norm / (want + 1e-6)) * scale
+    assert abs(float(norm) - want) <= 2.0 ** -23 * want + R.tiny(F32)
+    for o, t in zip(outs, (g, small)):
+        R.close(o, t.double().cpu() * by, 3 * 2.0 ** -24 * t.double().cpu().abs() * by + 2 * R.tiny(F32), "out")
