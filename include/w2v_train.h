@@ -132,10 +132,11 @@ size_t w2v_op_grad_clip_workspace(int n);
  * grads, outs, counts (elements), types: HOST arrays [n] (of device pointers,
  * the first two), read during the call; an output has its gradient's type.
  * scale (> 0) undoes a loss scale; max_norm = INFINITY only scales.  norm_dev:
- * one fp32, on the device.  counts below 2^33 each.  The sum is fp64.  If the norm is not finite,
- * nothing is clipped (outs = grads scale), so that a caller that reads norm_dev
- * can drop the step.  outs[i] may be grads[i] (in place); otherwise no tensor
- * may overlap another one.  Empty tensors are allowed.
+ * one fp32, on the device.  counts below 2^33 each.  The sum is fp64.  If the norm
+ * is not finite, or past fp32's range and so written as infinity, nothing is clipped
+ * (outs = grads scale): a caller that reads norm_dev can drop the step.  outs[i] may
+ * be grads[i] (in place); otherwise no tensor may overlap another one.  Empty tensors
+ * are allowed.
  * Errors: W2V_EINVAL (null or misaligned pointer, type, overlap, scale,
  * max_norm <= 0 or NaN, ws_bytes too small), W2V_ESHAPE (n or a count out of
  * range), W2V_ENOMEM (host), W2V_ECUDA. */

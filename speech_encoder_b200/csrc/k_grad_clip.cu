@@ -216,9 +216,10 @@ grad_scale_kernel(const __grid_constant__ ClipTable t, const double* __restrict_
   double s = 0.0;
   for (int i = threadIdx.x; i < partials; i += kClipThreads) s += partial[i];
   const double norm = sqrt(block_sum(s)) * fabs(static_cast<double>(scale));
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
+  const float written = static_cast<float>(norm);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = written;
   double by = static_cast<double>(max_norm) / (norm + 1e-6);
-  if (!(by < 1.0) || !(norm < INFINITY)) by = 1.0;  // not clipped, or not a finite norm
+  if (!(by < 1.0) || !(written < INFINITY)) by = 1.0;  // not clipped, or no finite norm for the caller to read
   by *= static_cast<double>(scale);
   // A factor below 2^-126 (a norm near fp32's end) would keep but a few bits as an fp32.
   const float lift = by < 0x1p-126 ? 0x1p-126f : 1.0f;

@@ -403,3 +403,14 @@ def test_grad_clip_factors_below_fp32(scale, max_norm):
     assert abs(float(norm) - want) <= 2.0 ** -23 * want + R.tiny(F32)
     for o, t in zip(outs, (g, small)):
         R.close(o, t.double().cpu() * by, 3 * 2.0 ** -24 * t.double().cpu().abs() * by + 2 * R.tiny(F32), "out")
+
+
+def test_grad_clip_norm_past_fp32():
+    """A norm that fp64 holds and fp32 does not is written as infinity, and clips nothing, as any infinite one."""
+    g = torch.full((5000,), 3e38, device="cuda")
+    out, norm = torch.empty_like(g), torch.empty(1, device="cuda")
+    B.w2v_op_grad_clip([g], [out], 0.5, 1.0, norm)
+    assert float(norm) == math.inf and torch.equal(out, g * 0.5)
+    B.w2v_op_grad_clip([g], [out], 2.0 ** -20, 1.0, norm)  # 2e34 after unscaling: clipped again
+    want = 3e38 * 2.0 ** -20 * math.sqrt(5000)
+    assert abs(float(norm) / want - 1) < 1e-6 and abs(float(out[7]) * math.sqrt(5000) - 1) < 1e-6
