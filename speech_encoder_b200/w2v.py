@@ -364,8 +364,11 @@ def w2v_op_wait_probe(err, limit_ns: int, stream=None) -> int:
 # for few interpreter steps: on short clips they take longer than the kernels.
 
 
-def _refuse(what: str):
-    raise W2VError(W2V_EINVAL, what)
+def _refuse(what: str, code: int = W2V_EINVAL):
+    raise W2VError(code, what)
+
+
+_INT_MAX = 2 ** 31 - 1  # ctypes passes a larger size without its upper bits
 
 
 _TYPES: dict = {}  # torch's element types -> the library's codes
@@ -435,6 +438,8 @@ def _attention_shape(qkv, outs, grads, lse, err, frames) -> w2v_attention_shape:
     if len(shape) != 3 or shape[2] == 0 or shape[2] % 64:
         _refuse("attention: q is not [batch, T, H * 64]")
     batch, T, width = shape
+    if batch > _INT_MAX or T > _INT_MAX or width > _INT_MAX:
+        _refuse("attention: q is too large", W2V_ESHAPE)
     rows = qkv + outs + grads
     _on_current_device("attention", rows + ((lse, err) if frames is None else (lse, err, frames)))
     for t in rows:
@@ -500,6 +505,8 @@ def w2v_op_layernorm_fwd(x, y, gamma, beta, eps: float, act: int, mean, rstd, st
     if len(shape) != 2:
         _refuse("layernorm: x is not [rows, cols]")
     rows, cols = shape
+    if cols > _INT_MAX:
+        _refuse("layernorm: too many columns", W2V_ESHAPE)
     _on_current_device("layernorm", (x, y, gamma, beta, mean, rstd))
     _norm_vectors(cols, (gamma, beta))
     _norm_vectors(rows, (mean, rstd))
@@ -522,6 +529,8 @@ def w2v_op_layernorm_bwd(dy, x, gamma, beta, mean, rstd, act: int, dres, dx, dga
     if len(shape) != 2:
         _refuse("layernorm: x is not [rows, cols]")
     rows, cols = shape
+    if cols > _INT_MAX:
+        _refuse("layernorm: too many columns", W2V_ESHAPE)
     tensors = (dy, x, gamma, beta, mean, rstd, dx, dgamma, dbeta)
     _on_current_device("layernorm", tensors if dres is None else tensors + (dres,))
     _norm_vectors(cols, (gamma, beta, dgamma, dbeta))

@@ -1,4 +1,5 @@
-"""The Python binding of the operators for training, without a GPU: which stream owns a workspace of its own."""
+"""The Python binding of the operators for training, without a GPU: which stream owns a workspace of its own, and
+sizes that do not fit the library's integers."""
 import contextlib
 
 import pytest
@@ -34,3 +35,26 @@ def test_workspace_belongs_to_the_stream_of_the_call(monkeypatch, stream, kind):
     pointer, nbytes, owner = B._workspace(None, 256, torch.device("cpu"), stream)
     assert pointer == owner.data_ptr() and nbytes == 256
     assert [(s.kind, s.cuda_stream) for s in entered] == [(kind, B._stream(stream))]
+
+
+@pytest.mark.parametrize("shape", [(1, (1 << 32) + 512), (3, 1 << 31)])
+def test_layernorm_rows_past_32_bits_are_refused(shape):
+    """Their size would reach the library without its upper bits: 2^32 + 512 columns as 512."""
+    x = torch.empty(shape, device="meta", dtype=torch.float16)
+    v, s = torch.empty(shape[1], device="meta"), torch.empty(shape[0], device="meta")
+    with pytest.raises(B.W2VError, match="columns") as e:
+        B.w2v_op_layernorm_fwd(x, x, v, v, 1e-5, 0, s, s)
+    assert e.value.code == B.W2V_ESHAPE
+    with pytest.raises(B.W2VError, match="columns"):
+        B.w2v_op_layernorm_bwd(x, x, v, v, s, s, 0, None, x, v, v)
+
+
+@pytest.mark.parametrize("shape", [((1 << 32) + 1, 1, 64), (1, (1 << 32) + 2, 64), (1, 1, 64 << 32)])
+def test_attention_sizes_past_32_bits_are_refused(shape):
+    q = torch.empty(shape, device="meta", dtype=torch.float16)
+    lse, err = torch.empty(shape[0], shape[2] // 64, shape[1], device="meta"), torch.empty(1, device="meta", dtype=torch.int32)
+    with pytest.raises(B.W2VError, match="large") as e:
+        B.w2v_op_attention_fwd(q, q, q, q, lse, err)
+    assert e.value.code == B.W2V_ESHAPE
+    with pytest.raises(B.W2VError, match="large"):
+        B.w2v_op_attention_bwd(q, q, q, q, q, lse, q, q, q, err)
