@@ -22,9 +22,9 @@ extern "C" {
  * (res_f32 = 1) or NULL; out [M][N] fp16 or fp32 (out_f32); act 0 none,
  * 1 exact GELU, 2 tanh GELU.  This is the contraction of every projection in
  * the encoder blocks (README "Recipe" table: q/k/v/out projections,
- * intermediate_dense, output_dense) and of the CTC head.  B is read as weights
- * are: from before the kernel queued just ahead on the stream has ended, so B must
- * not be that kernel's output (A and residual may be).  bn = 0 picks the
+ * intermediate_dense, output_dense) and of the CTC head.  B and bias are read as
+ * weights, from before the kernel queued just ahead on the stream has ended, so
+ * neither may be that kernel's output (A and residual may be).  bn = 0 picks the
  * tile width and split-K factor; otherwise bn (32/64/128/192/256) and splits
  * are forced: splits 1..8 (<= K/64) divides the K blocks among a cluster of
  * `splits` CTAs whose partial sums are reduced in distributed shared memory;
