@@ -52,6 +52,7 @@ typedef struct {
  * (the plain SDPA of w2v_op_attention at every clip's true length), and
  * lse [batch][H][T] (fp32), the natural logarithm of each row's sum of
  * exponentials, which the backward pass recomputes the probabilities from.
+ * out may be q, with the same strides (a forward pass without a backward one).
  * Rows past a clip's frames are written: out 0, lse -infinity; what the inputs
  * hold there, NaN included, is not used.  err_dev as in w2v_ops.h.
  * A row of a clip's own frames with a score that is NaN or +infinity, or with

@@ -116,7 +116,10 @@ extern "C" int w2v_op_attention_fwd(const w2v_attention_shape* shape, const void
       !aligned_to(err_dev, 4))
     return W2V_EINVAL;
   Operands o;
-  for (const void* p : {q, k, v}) o.clips(false, p, a, a.qkv_ld, a.qkv_bs);
+  // (a CTA reads the rows of q that it writes, and no other: out may be q)
+  const bool in_place = q == out && a.qkv_ld == a.out_ld && a.qkv_bs == a.out_bs;
+  if (!in_place) o.clips(false, q, a, a.qkv_ld, a.qkv_bs);
+  for (const void* p : {k, v}) o.clips(false, p, a, a.qkv_ld, a.qkv_bs);
   if (a.frames) o.bytes(false, a.frames, 4 * static_cast<int64_t>(a.batch));
   o.clips(true, out, a, a.out_ld, a.out_bs);
   o.bytes(true, lse, 4 * static_cast<int64_t>(a.batch) * a.H * a.T);

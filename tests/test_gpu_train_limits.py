@@ -238,6 +238,26 @@ def test_attention_gradients_over_their_operands_are_refused():
         B.w2v_op_attention_fwd(q, k, v, v, lse, err)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("frames", [None, [300, 0, 129, 128, 64, 1]])
+def test_attention_output_over_its_queries(frames, dtype):
+    """Without a backward pass to come, out may take the place of q (here, in a fused projection's rows)."""
+    gen = torch.Generator().manual_seed(16)
+    qkv = torch.randn(6, 300, 3, 192, generator=gen).to(dtype).cuda()
+    fr = None if frames is None else torch.tensor(frames, dtype=torch.int32, device="cuda")
+    out, err = torch.empty(6, 300, 3, 192, dtype=dtype, device="cuda")[:, :, 0], _err()
+    lse, again = torch.empty(2, 6, 3, 300, device="cuda")
+    q, k, v = (qkv[:, :, i] for i in range(3))
+    B.w2v_op_attention_fwd(q, k, v, out, lse, err, frames=fr)
+    kept = qkv[:, :, 1:].clone()
+    B.w2v_op_attention_fwd(q, k, v, q, again, err, frames=fr)
+    assert torch.equal(q, out) and torch.equal(lse, again) and torch.equal(qkv[:, :, 1:], kept)
+    assert int(err.item()) == 0
+    for args in ((q, q, v), (q, k, q)):  # as keys or values it is read by every row
+        with pytest.raises(B.W2VError):
+            B.w2v_op_attention_fwd(*args, q, lse, err)
+
+
 # ------------------------------------------------------- GELU over its whole range
 
 

@@ -38,6 +38,8 @@ def test_attention_outputs_over_other_operands(T):
         for other in set(FWD) - {out}:
             a = _apart(FWD)
             for at in (a[other], a[other] + (last if other in ("q", "k", "v", "out") else 0)):
+                if (out, other, at) == ("out", "q", a["q"]):
+                    continue  # in place: allowed
                 assert _fwd(s, dict(a, **{out: at})) == B.W2V_EINVAL, (out, other)
     for out in ("dq", "dk", "dv", "err") + (("ws",) if T > 128 else ()):
         for other in set(BWD) - {out} - (set() if T > 128 else {"ws"}):
