@@ -92,8 +92,8 @@ int w2v_op_attention_bwd(const w2v_attention_shape* shape, const void* dout, con
  * none, 1 exact GELU, 2 tanh GELU), biased variance, rstd = 1 / sqrt(var + eps);
  * mean and rstd (fp32 [rows]) are kept for the backward pass.  In the exact GELU and
  * its slope Phi is within 3e-7; with an fp32 y Phi(-|z|) is within 2^-19 + z^2 2^-23
- * of its own value up to |z| = 13, and with a 16-bit y within 2^-13.  x_type and y_type are equal, or x is fp32
- * and y fp16 or bf16 (the fp32 residual stream
+ * of its own value up to |z| = 13, and with a 16-bit y within 2^-13.  x_type and
+ * y_type are equal, or x is fp32 and y fp16 or bf16 (the fp32 residual stream
  * normalised for the next projection).  x_ld and y_ld: elements between rows,
  * >= cols; any alignment of the element type (rows of 16-byte multiples on
  * 16-byte boundaries are the fast case).  gamma, beta: fp32 [cols].

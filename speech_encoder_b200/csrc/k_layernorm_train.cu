@@ -165,8 +165,8 @@ struct NormalTail;
 
 // Results of 16 bits: degree 6, the smallest largest excess over absolute and relative
 // bounds of 1 : 1000 (6.4e-8 and 6.4e-5).  Measured over [-13, 13]: the slope within
-// 2.5e-7, and f, rounded, within 1.16 half steps of fp16 and 1.03 of bf16 (a polynomial
-// for the absolute error alone was up to 2.9 and, at -8, 18 off).
+// 2.5e-7, and f, rounded, within 1.16 half steps of fp16 and 1.03 of bf16 (2.9 and 18
+// with a polynomial of degree 5 for the absolute error alone).
 template <>
 struct NormalTail<false> {
   static constexpr float p = 0.2925f;
