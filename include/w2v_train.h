@@ -57,8 +57,9 @@ typedef struct {
  * hold there, NaN included, is not used.  err_dev as in w2v_ops.h.
  * A row of a clip's own frames with a score that is NaN or +infinity, or with
  * none above -infinity, has no softmax: its out and lse are NaN.
- * Scores, softmax and sums are fp32; the probabilities are rounded to dtype for
- * the product with v.
+ * Scores, softmax and sums are fp32 (an exponential within 3e-6 of itself, and so
+ * lse within 3e-6 beside the scores' own roundings); the probabilities are rounded to
+ * dtype for the product with v.
  * Errors: W2V_EINVAL (null or misaligned pointer, dtype, strides, overlap),
  * W2V_ESHAPE (batch, T or H < 1, T or the number of tiles too large), W2V_ECUDA. */
 int w2v_op_attention_fwd(const w2v_attention_shape* shape, const void* q, const void* k, const void* v, void* out,
